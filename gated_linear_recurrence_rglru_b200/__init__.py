@@ -10,7 +10,9 @@ and Google RecurrentGemma", "Core Components of Griffin", 1. RG-LRU). It is
 computed by hand-written CUDA kernels behind a C ABI; this package is the thin
 Python binding of that library (_abi.py). rglru_block_fwd adds the recurrent
 block around the layer (input and gate projections, GeLU gating, output
-projection).
+projection). attention.py binds the local attention beside it
+(include/rglru_attn.h): norms and rotation of queries and keys, attention over
+a sliding window with sinks, and one token's attention over a paged cache.
 
 The library is loaded on first use of any binding name below, and that use
 raises ImportError if the library is missing (there is no CPU path).
@@ -21,9 +23,15 @@ __all__ = ["rglru_fwd", "rglru_fwd_noalloc", "rglru_decode_step", "rglru_bwd", "
            "fwd_workspace_bytes", "bwd_workspace_bytes", "block_fwd_workspace_bytes",
            "fwd_launches", "bwd_launches", "decode_launches", "FwdOptions", "RGLRUError",
            "status_str", "version", "LIB_PATH", "ALGO_AUTO", "ALGO_GENERIC", "ALGO_TENSOR"]
+_ATTENTION = ("rglru_qk_norm_rope_fwd", "rglru_qk_norm_rope_append", "rglru_qk_norm_rope_bwd",
+              "rglru_local_attn_fwd", "rglru_local_attn_bwd", "rglru_paged_attn_decode")
+__all__ += _ATTENTION
 
 
 def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        return getattr(attention, name)
     if name in __all__:
         from . import _abi
         return getattr(_abi, name)

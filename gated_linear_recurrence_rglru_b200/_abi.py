@@ -25,7 +25,10 @@ EXPORTED = (
     "rglru_fwd_algo", "rglru_decode_step", "rglru_decode_step_algo", "rglru_fwd_launches",
     "rglru_fwd_noalloc", "rglru_decode_launches", "rglru_fwd_ex", "rglru_bwd",
     "rglru_bwd_workspace_bytes", "rglru_bwd_launches", "rglru_block_fwd",
-    "rglru_block_fwd_workspace_bytes",
+    "rglru_block_fwd_workspace_bytes", "rglru_qk_norm_rope_fwd", "rglru_qk_norm_rope_append",
+    "rglru_qk_norm_rope_bwd", "rglru_qk_norm_rope_bwd_workspace_bytes", "rglru_local_attn_fwd",
+    "rglru_local_attn_bwd", "rglru_local_attn_bwd_workspace_bytes", "rglru_paged_attn_decode",
+    "rglru_paged_attn_decode_workspace_bytes",
 )
 
 

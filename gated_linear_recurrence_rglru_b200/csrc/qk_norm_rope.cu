@@ -1,0 +1,400 @@
+// Norms of queries and keys per head and their position rotation, in one pass
+// over HBM: forward, the serving form that writes a paged cache, and backward
+// (include/rglru_attn.h).
+//
+//   n = x * r * w,  r = rsqrt(mean(x^2) + eps)
+//   y_i = n_i cos - n_j sin,  y_j = n_j cos + n_i sin,  j = i + rot/2, i < rot/2
+//
+// Backward, with g = the rotation's transpose applied to dy:
+//   dw = sum over rows of g * x r,   dx = r (g w - x r^2 mean(g w x))
+//
+// Bound by HBM: x (and dy) read once, y (dx) written once. One warp takes one
+// token and a run of its heads; a lane holds 8 consecutive elements of a row
+// (16 bytes of bf16), a row is dh/8 lanes, so narrow heads put several rows in
+// a warp. Norm sums are warp shuffles; the rotation's partner sits rot/16 lanes
+// away at the same place of its lane (rot is a multiple of 16), one shuffle.
+// Sine and cosine are formed once per token and warp for all of the run's
+// heads. The angle of pair i is position * phase[i] in 64-bit integers, phase
+// a fraction of a turn times 2^64: the product modulo 2^64 is the exact
+// position within the turn, so far positions keep full precision without
+// 64-bit floating point (the phase's own rounding, 2^-65 of a turn, times
+// 2^31 positions is 2^-34 of a turn).
+#include "attn_kernels.h"
+#include "common.cuh"
+
+namespace rglru {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxBlocks = 148 * 6;
+constexpr int kBwdBlocks = 148 * 4;   // each leaves one partial sum of dw
+
+struct Row8 {
+  float v[8];
+};
+
+__device__ __forceinline__ Row8 load8(const float *p) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+__device__ __forceinline__ Row8 load8(const __nv_bfloat16 *p) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  Row8 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    r.v[2 * e] = __uint_as_float(w[e] << 16);
+    r.v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store8(float *p, const Row8 &r) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Row8 &r) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(r.v[2 * e], r.v[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 elements moved as they are (v into its cache).
+__device__ __forceinline__ void copy8(float *d, const float *s) {
+  reinterpret_cast<float4 *>(d)[0] = __ldg(reinterpret_cast<const float4 *>(s));
+  reinterpret_cast<float4 *>(d)[1] = __ldg(reinterpret_cast<const float4 *>(s) + 1);
+}
+__device__ __forceinline__ void copy8(__nv_bfloat16 *d, const __nv_bfloat16 *s) {
+  *reinterpret_cast<uint4 *>(d) = __ldg(reinterpret_cast<const uint4 *>(s));
+}
+
+template <int LPR> __device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// What a lane needs of the rotation at one token: whether its elements turn,
+// the lane that holds their partners, and (cos, +-sin) of each. The first of a
+// pair takes -sin (forward), the second +sin; `back` turns the other way.
+struct Turn {
+  float c[8], s[8];
+  bool on;
+  int partner;
+};
+
+__device__ __forceinline__ void set_turn(Turn &t, const unsigned long long *phase, int pos, int e0,
+                                         int half, bool back) {
+  if (!t.on) return;
+  const bool first = e0 < half;
+  const int i0 = first ? e0 : e0 - half;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned long long turn =
+        phase[i0 + e] * static_cast<unsigned long long>(static_cast<long long>(pos));
+    // the top 32 bits as a signed fraction of a turn, -1/2 .. 1/2
+    const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
+    sincospif(x, &t.s[e], &t.c[e]);   // angle = pi x, x = 2 * fraction
+    if (first != back) t.s[e] = -t.s[e];
+  }
+}
+
+__device__ __forceinline__ void rotate(Row8 &n, const Turn &t) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float o = __shfl_sync(0xFFFFFFFFu, n.v[e], t.partner);
+    if (t.on) n.v[e] = n.v[e] * t.c[e] + o * t.s[e];
+  }
+}
+
+// A warp's place: LPR lanes a row (dh/8 of them in use), 32/LPR rows at once.
+template <int LPR> struct Place {
+  int sub, e0;
+  bool in;
+  __device__ Place(int lane, int dh) : sub(lane / LPR), e0((lane % LPR) * 8), in(e0 < dh) {}
+};
+
+template <int LPR> __device__ __forceinline__ Turn make_turn(int lane, int e0, int rot) {
+  Turn t;
+  const int half = rot / 2;
+  t.on = e0 < rot;
+  t.partner = !t.on ? lane : e0 < half ? lane + half / 8 : lane - half / 8;
+  return t;
+}
+
+__device__ __forceinline__ void stage_phases(unsigned long long *dst, const QkArgs &p) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) dst[i] = p.phase[i];
+}
+
+template <typename T>
+__device__ __forceinline__ Row8 weights(const void *w, int e0, bool in) {
+  Row8 r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.v[e] = 1.0f;
+  if (w != nullptr && in) r = load8(static_cast<const T *>(w) + e0);
+  return r;
+}
+
+// Forward (kAppend: k and v rows go to the cache). Work item: one token and one
+// of n_runs runs of `run` heads of the list q heads, k heads.
+template <typename T, int LPR, bool kAppend>
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkArgs p,
+                                                          int run, int n_runs) {
+  __shared__ unsigned long long phase[kMaxPairs];
+  stage_phases(phase, p);
+  __syncthreads();
+  constexpr int R = 32 / LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Place<LPR> at(lane, p.dh);
+  const Row8 wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
+  Turn turn = make_turn<LPR>(lane, at.e0, p.rot);
+  const int heads = p.Hq + p.Hkv;
+  const float inv = 1.0f / static_cast<float>(p.dh);
+  const long long items = static_cast<long long>(p.B) * p.T * n_runs;
+  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items;
+       it += static_cast<long long>(gridDim.x) * kWarps) {
+    const long long tok = it / n_runs;
+    const int h0 = static_cast<int>(it % n_runs) * run;
+    const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
+    const int pos = p.positions ? __ldg(p.positions + tok) : t;
+    long long slot = 0;
+    bool stored = true;                                 // whether the token has a cache slot
+    if (kAppend) {
+      if (pos < 0) continue;                            // padding (the warp's one token)
+      const int pg = pos / p.page_size;
+      const int page = pg < p.max_pages
+                           ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pg)
+                           : -1;
+      stored = page >= 0 && page < p.num_pages;
+      if (!stored && p.dev_status && lane == 0)
+        atomicCAS(p.dev_status, 0, RGLRU_ERR_INVALID_ARG);
+      slot = (static_cast<long long>(page) * p.page_size + pos % p.page_size) * p.Hkv;
+    }
+    set_turn(turn, phase, pos, at.e0, p.rot / 2, false);
+    const int h1 = min(h0 + run, heads);
+#pragma unroll 2
+    for (int h = h0; h < h1; h += R) {
+      const int hh = h + at.sub;
+      const bool live = at.in && hh < h1;
+      const bool is_q = hh < p.Hq;
+      const int hk = hh - p.Hq;
+      Row8 x = {};
+      if (live) {
+        const T *src = is_q ? static_cast<const T *>(p.q.p) + b * p.q.sb + t * p.q.st + hh * p.q.sh
+                            : static_cast<const T *>(p.k.p) + b * p.k.sb + t * p.k.st + hk * p.k.sh;
+        x = load8(src + at.e0);
+      }
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
+      const float r = rsqrtf(row_sum<LPR>(ss) * inv + p.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.v[e] *= r * (is_q ? wq.v[e] : wk.v[e]);
+      rotate(x, turn);
+      if (!live) continue;
+      if (is_q) {
+        store8(static_cast<T *>(p.q_out) + (tok * p.Hq + hh) * p.dh + at.e0, x);
+      } else if (!kAppend) {
+        store8(static_cast<T *>(p.k_out) + (tok * p.Hkv + hk) * p.dh + at.e0, x);
+      } else if (stored) {
+        store8(static_cast<T *>(p.k_cache) + (slot + hk) * p.dh + at.e0, x);
+        copy8(static_cast<T *>(p.v_cache) + (slot + hk) * p.dh + at.e0,
+              static_cast<const T *>(p.v.p) + b * p.v.sb + t * p.v.st + hk * p.v.sh + at.e0);
+      }
+    }
+  }
+}
+
+// Backward; each block leaves its sums of dw_q and dw_k in partial[block][2][dh].
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant__ QkArgs p,
+                                                          int run, int n_runs, float *partial) {
+  __shared__ unsigned long long phase[kMaxPairs];
+  __shared__ float sums[kWarps][2][256 + 8];
+  stage_phases(phase, p);
+  __syncthreads();
+  constexpr int R = 32 / LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Place<LPR> at(lane, p.dh);
+  const Row8 wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
+  Turn turn = make_turn<LPR>(lane, at.e0, p.rot);
+  Row8 dwq = {}, dwk = {};
+  const int heads = p.Hq + p.Hkv;
+  const float inv = 1.0f / static_cast<float>(p.dh);
+  const long long items = static_cast<long long>(p.B) * p.T * n_runs;
+  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items;
+       it += static_cast<long long>(gridDim.x) * kWarps) {
+    const long long tok = it / n_runs;
+    const int h0 = static_cast<int>(it % n_runs) * run;
+    const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
+    const int pos = p.positions ? __ldg(p.positions + tok) : t;
+    set_turn(turn, phase, pos, at.e0, p.rot / 2, true);
+    const int h1 = min(h0 + run, heads);
+#pragma unroll 2
+    for (int h = h0; h < h1; h += R) {
+      const int hh = h + at.sub;
+      const bool live = at.in && hh < h1;
+      const bool is_q = hh < p.Hq;
+      const int hk = hh - p.Hq;
+      const long long row = is_q ? tok * p.Hq + hh : tok * p.Hkv + hk;
+      Row8 x = {}, g = {};
+      if (live) {
+        const T *src = is_q ? static_cast<const T *>(p.q.p) + b * p.q.sb + t * p.q.st + hh * p.q.sh
+                            : static_cast<const T *>(p.k.p) + b * p.k.sb + t * p.k.st + hk * p.k.sh;
+        x = load8(src + at.e0);
+        g = load8(static_cast<const T *>(is_q ? p.dq_out : p.dk_out) + row * p.dh + at.e0);
+      }
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
+      const float r = rsqrtf(row_sum<LPR>(ss) * inv + p.eps);
+      rotate(g, turn);
+      float gx = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = g.v[e] * (x.v[e] * r);
+        if (is_q)
+          dwq.v[e] += d;
+        else
+          dwk.v[e] += d;
+        g.v[e] *= is_q ? wq.v[e] : wk.v[e];
+        gx = fmaf(g.v[e], x.v[e], gx);
+      }
+      const float c = row_sum<LPR>(gx) * inv * r * r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g.v[e] = r * (g.v[e] - x.v[e] * c);
+      if (live) store8(static_cast<T *>(is_q ? p.q_out : p.k_out) + row * p.dh + at.e0, g);
+    }
+  }
+  // rows of one warp (lanes LPR apart hold the same elements), then the warps
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) {
+      dwq.v[e] += __shfl_xor_sync(0xFFFFFFFFu, dwq.v[e], o);
+      dwk.v[e] += __shfl_xor_sync(0xFFFFFFFFu, dwk.v[e], o);
+    }
+    if (at.sub == 0 && at.in) {
+      sums[warp][0][at.e0 + e] = dwq.v[e];
+      sums[warp][1][at.e0 + e] = dwk.v[e];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.dh; i += kThreads) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += sums[w][i / p.dh][i % p.dh];
+    partial[static_cast<size_t>(blockIdx.x) * 2 * p.dh + i] = s;
+  }
+}
+
+// dw[i] = sum over the blocks of partial[block][i], in double: one warp a
+// column, lanes over the blocks, a fixed order.
+__global__ void __launch_bounds__(kThreads) qk_dw_kernel(const float *__restrict__ partial,
+                                                         int blocks, int dh, float *dw_q,
+                                                         float *dw_k) {
+  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= 2 * dh) return;
+  double s = 0.0;
+  for (int b = lane; b < blocks; b += 32) s += partial[static_cast<size_t>(b) * 2 * dh + i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  float *dst = i < dh ? dw_q : dw_k;
+  if (lane == 0 && dst != nullptr) dst[i % dh] = static_cast<float>(s);
+}
+
+// Heads per work item: all of a token's (its sines are then formed once), or
+// fewer when that leaves warps without work.
+int heads_per_item(long long tokens, int heads, int rows_at_once) {
+  const long long warps = 148ll * 4 * kWarps;
+  int n_runs = 1;
+  if (tokens < warps) n_runs = static_cast<int>((warps + tokens - 1) / (tokens > 0 ? tokens : 1));
+  const int most = ceil_div(heads, rows_at_once);
+  if (n_runs > most) n_runs = most;
+  const int run = ceil_div(heads, n_runs);
+  return ceil_div(run, rows_at_once) * rows_at_once;
+}
+
+int lanes_per_row(int dh) {
+  int l = 1;
+  while (l * 8 < dh) l *= 2;
+  return l;
+}
+
+template <typename T, int LPR>
+cudaError_t launch(const QkArgs &p, int mode, float *partial, int blocks, int run, int n_runs,
+                   cudaStream_t st) {
+  if (mode == 0)
+    qk_fwd_kernel<T, LPR, false><<<blocks, kThreads, 0, st>>>(p, run, n_runs);
+  else if (mode == 1)
+    qk_fwd_kernel<T, LPR, true><<<blocks, kThreads, 0, st>>>(p, run, n_runs);
+  else
+    qk_bwd_kernel<T, LPR><<<blocks, kThreads, 0, st>>>(p, run, n_runs, partial);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_lpr(const QkArgs &p, int mode, float *partial, int blocks, int run, int n_runs,
+                       cudaStream_t st) {
+  switch (lanes_per_row(p.dh)) {
+    case 1: return launch<T, 1>(p, mode, partial, blocks, run, n_runs, st);
+    case 2: return launch<T, 2>(p, mode, partial, blocks, run, n_runs, st);
+    case 4: return launch<T, 4>(p, mode, partial, blocks, run, n_runs, st);
+    case 8: return launch<T, 8>(p, mode, partial, blocks, run, n_runs, st);
+    case 16: return launch<T, 16>(p, mode, partial, blocks, run, n_runs, st);
+    default: return launch<T, 32>(p, mode, partial, blocks, run, n_runs, st);
+  }
+}
+
+int qk_blocks(int B, int T, int Hq, int Hkv, int dh, int most, int *run, int *n_runs) {
+  const int heads = Hq + Hkv;
+  *run = heads_per_item(static_cast<long long>(B) * T, heads, 32 / lanes_per_row(dh));
+  *n_runs = ceil_div(heads, *run);
+  const long long items = static_cast<long long>(B) * T * *n_runs;
+  const long long blocks = (items + kWarps - 1) / kWarps;
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+cudaError_t run_mode(const QkArgs &p, int io, int mode, cudaStream_t st) {
+  int run, n_runs;
+  const int blocks = qk_blocks(p.B, p.T, p.Hq, p.Hkv, p.dh, kMaxBlocks, &run, &n_runs);
+  return io == RGLRU_IO_F32 ? launch_lpr<float>(p, mode, nullptr, blocks, run, n_runs, st)
+                            : launch_lpr<__nv_bfloat16>(p, mode, nullptr, blocks, run, n_runs, st);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_fwd(const QkArgs &p, int io, cudaStream_t st) { return run_mode(p, io, 0, st); }
+
+cudaError_t launch_qk_append(const QkArgs &p, int io, cudaStream_t st) {
+  return run_mode(p, io, 1, st);
+}
+
+size_t qk_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int dh) {
+  int run, n_runs;
+  const int blocks = qk_blocks(B, T, Hq, Hkv, dh, kBwdBlocks, &run, &n_runs);
+  return static_cast<size_t>(blocks) * 2 * dh * sizeof(float);
+}
+
+cudaError_t launch_qk_bwd(const QkArgs &p, int io, void *ws, cudaStream_t st) {
+  int run, n_runs;
+  const int blocks = qk_blocks(p.B, p.T, p.Hq, p.Hkv, p.dh, kBwdBlocks, &run, &n_runs);
+  float *partial = static_cast<float *>(ws);
+  const cudaError_t e =
+      io == RGLRU_IO_F32 ? launch_lpr<float>(p, 2, partial, blocks, run, n_runs, st)
+                         : launch_lpr<__nv_bfloat16>(p, 2, partial, blocks, run, n_runs, st);
+  if (e != cudaSuccess || (p.dw_q == nullptr && p.dw_k == nullptr)) return e;
+  qk_dw_kernel<<<ceil_div(2 * p.dh, kWarps), kThreads, 0, st>>>(partial, blocks, p.dh, p.dw_q,
+                                                                p.dw_k);
+  return cudaGetLastError();
+}
+
+}  // namespace rglru
