@@ -290,9 +290,10 @@ int rglru_local_attn_fwd(const void *q, const rglru_strides *q_strides, const vo
   a.out = out;
   a.lse = lse;
   a.dev_status = dev_status;
-  return launch_attn_fwd_generic(a, io, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? RGLRU_OK
-             : RGLRU_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      attn_tc_supported(a, io) ? launch_attn_fwd_tc(a, s) : launch_attn_fwd_generic(a, io, s);
+  return e == cudaSuccess ? RGLRU_OK : RGLRU_ERR_CUDA;
 }
 
 size_t rglru_local_attn_bwd_workspace_bytes(int B, int T, int S, int Hq, int Hkv, int dh,
