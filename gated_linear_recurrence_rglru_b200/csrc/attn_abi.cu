@@ -308,7 +308,9 @@ size_t rglru_local_attn_bwd_workspace_bytes(int B, int T, int S, int Hq, int Hkv
   a.window = window;
   a.sinks = sinks;
   if (check_attn(&a, io) != RGLRU_OK) return 0;
-  return align_up(attn_bwd_generic_workspace_bytes(a), 256);
+  return align_up(attn_tc_supported(a, io) ? attn_bwd_tc_workspace_bytes(a)
+                                           : attn_bwd_generic_workspace_bytes(a),
+                  256);
 }
 
 int rglru_local_attn_bwd(const void *q, const rglru_strides *q_strides, const void *k,
@@ -355,9 +357,10 @@ int rglru_local_attn_bwd(const void *q, const rglru_strides *q_strides, const vo
   a.dk = dk;
   a.dv = dv;
   a.dev_status = dev_status;
-  return launch_attn_bwd_generic(a, io, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? RGLRU_OK
-             : RGLRU_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = attn_tc_supported(a, io) ? launch_attn_bwd_tc(a, workspace, s)
+                                                 : launch_attn_bwd_generic(a, io, workspace, s);
+  return e == cudaSuccess ? RGLRU_OK : RGLRU_ERR_CUDA;
 }
 
 }  // extern "C"

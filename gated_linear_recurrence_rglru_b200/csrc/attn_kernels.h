@@ -106,6 +106,8 @@ cudaError_t launch_attn_bwd_generic(const AttnArgs &p, int io, void *ws, cudaStr
 // Tensor-core kernels: bf16, heads 64, 128 or 256 wide.
 bool attn_tc_supported(const AttnArgs &p, int io);
 cudaError_t launch_attn_fwd_tc(const AttnArgs &p, cudaStream_t st);
+size_t attn_bwd_tc_workspace_bytes(const AttnArgs &p);
+cudaError_t launch_attn_bwd_tc(const AttnArgs &p, void *ws, cudaStream_t st);
 
 // ------------------------------------------------ one token over a paged cache
 

@@ -1,0 +1,638 @@
+// Windowed attention with sinks on the 5th-generation tensor core, backward
+// (include/rglru_attn.h), for bf16 heads 64, 128 or 256 wide.
+//
+//   P = 2^(S c - lse log2 e), dP = dO V^T, dS = P (dP - delta),
+//   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO
+//
+// Every block keeps 128 rows of one side resident and walks tiles of the other,
+// so each gradient is summed in TMEM in a fixed order, without atomics: query
+// rows against the keys they see (dQ), key rows against the queries that see
+// them, head by head over the group that shares the key head (dK, dV). Both
+// are one walk: with resident rows X, Y and walked tiles U, W
+//   query rows  X = Q, Y = dO, U = K, W = V;   key rows  X = K, Y = V, U = Q, W = dO
+//   S = X U^T,  dP = Y W^T,  first += dS U,  second += P W
+// (key rows hold S and dP transposed, lse and delta then vary along the columns
+// and are read from shared memory). dQ sums `first`; dK and dV are `first` and
+// `second`. 256-wide heads have no room in TMEM for both sums (2 x 256 of 512
+// columns): dK and dV are blocks of their own there, at the price of a second S.
+// Seven products (eight for 256-wide heads) instead of the five of one pass that
+// adds dQ up in memory by atomics, whose order would change the result.
+//
+// Warps 0-7 turn scores into weights, warp group g half of a tile's columns,
+// thread = row = TMEM lane; P and dS go back to TMEM as bf16 over the scores
+// they came from and are the A operand of their product. Warp 8 issues the TMA
+// copies, warp 9 the MMAs in an order that keeps the tensor core fed: the next
+// tile's S runs while dS is formed, and P of the next tile is formed during
+// `first` and dP.
+//
+// All kinds of a call are one grid, the key-row blocks first. Key rows' steps
+// are cut into pieces (PiecePlan), joined by attn_join_kernel.
+//
+// Every wait is bounded; on expiry the kernel records RGLRU_ERR_TIMEOUT (wait
+// site 8), drains what it issued and returns.
+#include "attn_tc.cuh"
+
+namespace rglru {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128;
+constexpr int kThreads = 320;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int kSite = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+  AttnArgs a;
+  PiecePlan pl;
+  const float *delta;
+  float *parts;
+  int n_qt;
+  unsigned n_kv;     // key-row blocks of one kind
+  int v8;            // gradients' rows may be stored 32 bytes at a time
+  float c;           // scale * log2 e
+};
+
+// kFirst: sum dS U; kSecond: sum P W.
+template <int DH, bool kFirst, bool kSecond> struct Cfg {
+  static constexpr int kBN = DH == 256 ? 64 : 128;         // rows of a walked tile
+  static constexpr int kNS = kFirst ? 1 : 2;               // score buffers
+  static constexpr int kNW = DH == 256 && kFirst ? 1 : 2;  // W buffers (U has two)
+  static constexpr int kXBytes = kBM * DH * 2;
+  static constexpr int kTile = kBN * DH * 2;
+  static constexpr int kOffY = kXBytes;
+  static constexpr int kOffU = kOffY + (kFirst ? kXBytes : 0);
+  static constexpr int kOffW = kOffU + 2 * kTile;
+  static constexpr int kOffStat = kOffW + kNW * kTile;     // [2][lse, delta][kBN]
+  static constexpr int kOffBar = kOffStat + 2 * 2 * kBN * 4;
+  static constexpr int kNumBars = 16;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffMisc + 16;
+  static constexpr int kTSecond = kFirst ? DH : 0;         // TMEM columns
+  static constexpr int kTS = kTSecond + (kSecond ? DH : 0);
+  static constexpr int kTdP = kTS + kNS * kBN;
+  static_assert(kSmem <= kMaxSmem && kTdP + (kFirst ? kBN : 0) <= 512, "shared memory, TMEM");
+};
+
+template <int DH> constexpr int smem_bytes() {
+  if constexpr (DH == 256)
+    return Cfg<256, true, false>::kSmem > Cfg<256, false, true>::kSmem ? Cfg<256, true, false>::kSmem
+                                                                      : Cfg<256, false, true>::kSmem;
+  else
+    return Cfg<DH, true, true>::kSmem;
+}
+
+// Where a block stands: its rows, and the walk over the other side.
+struct Walk {
+  int b, h, kvh;       // h: query rows only
+  int r0;              // first row
+  RowLens len;
+  int n;               // steps
+  KeyTiles kt;         // query rows
+  Steps st;            // key rows: steps first .. first + n - 1
+  int first;
+};
+
+// A step's head (key rows), and the first row of its tile.
+template <bool kKeys, int kBN> __device__ __forceinline__ void step_at(const Walk &w, int G, int i, int &h, int &t0) {
+  if (kKeys) {
+    const int x = w.first + i;
+    h = w.kvh * G + x / w.st.nq;
+    t0 = (w.st.q0 + x % w.st.nq) * kBN;
+  } else {
+    h = w.kvh;
+    t0 = w.kt.tile(i) * kBN;
+  }
+}
+
+__device__ __forceinline__ void bar_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int DH, bool kKeys, bool kFirst, bool kSecond>
+__device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, const CUtensorMap *my,
+                                     const CUtensorMap *mu, const CUtensorMap *mw, const Walk &wk,
+                                     bool whole_tile, size_t slot, unsigned char *sm) {
+  using C = Cfg<DH, kFirst, kSecond>;
+  constexpr int kBN = C::kBN, kHalf = kBN / 2;
+  const AttnArgs &p = prm.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.Hq / p.Hkv, off = p.S - p.T;
+  uint64_t *x_full = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
+  uint64_t *u_full = x_full + 1, *u_empty = u_full + 2;
+  uint64_t *w_full = u_empty + 2, *w_empty = w_full + 2;
+  uint64_t *s_full = w_empty + 2;                     // [kNS]
+  uint64_t *p_full = s_full + 2;                      // [kNS] P is in TMEM (kSecond) or S was read
+  uint64_t *dp_full = p_full + 2, *ds_full = dp_full + 1, *done = ds_full + 1;
+  static_assert(C::kNumBars >= 16, "barriers");
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
+  volatile int *abort = reinterpret_cast<volatile int *>(sm + C::kOffMisc + 4);
+  float *stat = reinterpret_cast<float *>(sm + C::kOffStat);
+  if (tid == 0) {
+    mbar_init(x_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&u_full[s], 1);
+      mbar_init(&u_empty[s], 1);
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 8);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto give_up = [&]() {
+    if (!*abort) {
+      if (p.dev_status) atomicCAS(p.dev_status, 0, RGLRU_ERR_TIMEOUT | (kSite << 8) |
+                                                       (static_cast<int>(blockIdx.x & 0x7FFFu) << 16));
+      *abort = 1;
+    }
+  };
+
+  if (warp == 8) {
+    // ============================ TMA producer ============================
+    if (lane == 0) {
+      const int xh = kKeys ? wk.kvh : wk.h;
+      mbar_arrive_expect_tx(x_full, C::kXBytes * (kFirst ? 2 : 1));
+      for (int c = 0; c < DH / 64; ++c) {
+        tma_load_4d(sm + c * (kBM * 128), mx, x_full, c * 64, wk.r0, xh, wk.b);
+        if (kFirst) tma_load_4d(sm + C::kOffY + c * (kBM * 128), my, x_full, c * 64, wk.r0, xh, wk.b);
+      }
+      int i = 0, w_issued = 0, u_issued = 0;
+      for (; i < wk.n; ++i) {
+        int h, t0;
+        step_at<kKeys, kBN>(wk, G, i, h, t0);
+        const int u = i & 1, w = i % C::kNW;
+        if (!mbar_wait(&u_empty[u], ((i >> 1) & 1) ^ 1, abort, kWaitNs)) {
+          give_up();
+          break;
+        }
+        mbar_arrive_expect_tx(&u_full[u], C::kTile);
+        for (int c = 0; c < DH / 64; ++c)
+          tma_load_4d(sm + C::kOffU + u * C::kTile + c * (kBN * 128), mu, &u_full[u], c * 64, t0, h, wk.b);
+        u_issued = i + 1;
+        if (!mbar_wait(&w_empty[w], ((i / C::kNW) & 1) ^ 1, abort, kWaitNs)) {
+          give_up();
+          break;
+        }
+        mbar_arrive_expect_tx(&w_full[w], C::kTile);
+        for (int c = 0; c < DH / 64; ++c)
+          tma_load_4d(sm + C::kOffW + w * C::kTile + c * (kBN * 128), mw, &w_full[w], c * 64, t0, h, wk.b);
+        w_issued = i + 1;
+      }
+      if (*abort) {
+        mbar_wait_drain(x_full, 0, kDrainNs);
+        for (int j = u_issued - 1; j >= 0 && j >= u_issued - 2; --j)
+          mbar_wait_drain(&u_full[j & 1], (j >> 1) & 1, kDrainNs);
+        for (int j = w_issued - 1; j >= 0 && j >= w_issued - C::kNW; --j)
+          mbar_wait_drain(&w_full[j % C::kNW], (j / C::kNW) & 1, kDrainNs);
+      }
+    }
+  } else if (warp == 9) {
+    // ============================= MMA issuer =============================
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t id_o = idesc_bf16_f32(kBM, DH, false, true);
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
+          give_up();
+          ok = false;
+        }
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      // rows (K-major, resident) times tile (K-major): D = R T^T over DH
+      auto scores = [&](uint32_t d, int off_rows, int off_tile) {
+        const uint64_t ad = sdesc_sw128(smem_u32(sm + off_rows), 16, 1024);
+        const uint64_t bd = sdesc_sw128(smem_u32(sm + off_tile), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k)
+          mma_bf16(d, ad + static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * (kBM * 128)) >> 4),
+                   bd + static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4), id_s,
+                   k > 0 ? 1u : 0u);
+      };
+      // weights in TMEM (each half of the columns at the start of its scores)
+      // times tile (MN-major): D += A T
+      auto product = [&](uint32_t d, uint32_t a, int off_tile, bool add) {
+        const uint64_t bd = sdesc_sw128(smem_u32(sm + off_tile), kBN * 128, 1024);
+#pragma unroll
+        for (int k = 0; k < kBN / 16; ++k)
+          mma_bf16_ts(d, a + (k / (kHalf / 16)) * kHalf + (k % (kHalf / 16)) * 8,
+                      bd + static_cast<uint64_t>((k * 16 * 128) >> 4), id_o, (add || k > 0) ? 1u : 0u);
+      };
+      auto u_at = [&](int i) { return C::kOffU + (i & 1) * C::kTile; };
+      auto w_at = [&](int i) { return C::kOffW + (i % C::kNW) * C::kTile; };
+      auto issue_s = [&](int i) {
+        if (!wait(&u_full[i & 1], (i >> 1) & 1)) return;
+        scores(tmem + C::kTS + (i % C::kNS) * kBN, 0, u_at(i));
+        mma_commit(&s_full[i % C::kNS]);
+        if (!kFirst) mma_commit(&u_empty[i & 1]);
+      };
+      auto issue_dp = [&](int i) {
+        if (!wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+        scores(tmem + C::kTdP, C::kOffY, w_at(i));
+        mma_commit(dp_full);
+        if (!kSecond) mma_commit(&w_empty[i % C::kNW]);
+      };
+      auto issue_second = [&](int i) {
+        if (!kFirst && !wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+        product(tmem + C::kTSecond, tmem + C::kTS + (i % C::kNS) * kBN, w_at(i), i > 0);
+        mma_commit(&w_empty[i % C::kNW]);
+      };
+      wait(x_full, 0);
+      if (ok) issue_s(0);
+      if (kFirst && ok) issue_dp(0);
+      for (int i = 0; i < wk.n && ok; ++i) {
+        if (!kFirst) {
+          if (i + 1 < wk.n) issue_s(i + 1);
+          if (ok && wait(&p_full[i & 1], (i >> 1) & 1)) issue_second(i);
+          continue;
+        }
+        // P is in place, or S was read: the score columns are free after `second`
+        if (!wait(&p_full[0], i & 1)) break;
+        if (kSecond) issue_second(i);
+        if (ok && i + 1 < wk.n) issue_s(i + 1);
+        if (ok && wait(ds_full, i & 1)) {
+          product(tmem, tmem + C::kTdP, u_at(i), i > 0);
+          mma_commit(&u_empty[i & 1]);
+          if (i + 1 < wk.n) issue_dp(i + 1);
+        }
+      }
+      mma_commit(done);
+      if (*abort) mbar_wait_drain(done, 0, kDrainNs);
+    }
+  } else {
+    // =============================== weights ==============================
+    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int r = wk.r0 + row;                             // this thread's query or key
+    const int nq = wk.len.nq, nk = wk.len.nk;
+    float row_lse = 0.0f, row_delta = 0.0f;
+    if (!kKeys && r < nq) {
+      const long long x = (static_cast<long long>(wk.b) * p.Hq + wk.h) * p.T + r;
+      row_lse = __ldg(p.lse + x) * kLog2e;
+      if (kFirst) row_delta = __ldg(prm.delta + x);
+    }
+    // key rows: lse (threads 0..) and delta (threads 128..) of a step's queries
+    auto load_stat = [&](int i) -> float {
+      const bool second = tid >= 128;
+      const int c = tid & 127;
+      if (c >= kBN || (second && !kFirst)) return 0.0f;
+      int h, t0;
+      step_at<kKeys, kBN>(wk, G, i, h, t0);
+      if (t0 + c >= nq) return 0.0f;                       // masked
+      const long long x = (static_cast<long long>(wk.b) * p.Hq + h) * p.T + t0 + c;
+      return second ? __ldg(prm.delta + x) : __ldg(p.lse + x) * kLog2e;
+    };
+    auto store_stat = [&](int i, float v) {
+      const int c = tid & 127;
+      if (c < kBN) stat[((i & 1) * 2 + (tid >> 7)) * kBN + c] = v;
+    };
+    if (kKeys) store_stat(0, load_stat(0));
+    bool ok = true;
+    for (int i = 0; i < wk.n; ++i) {
+      int h, t0;
+      step_at<kKeys, kBN>(wk, G, i, h, t0);
+      float next = 0.0f;
+      if (kKeys) {
+        bar_sync_softmax();                                // this step's stats are there
+        if (i + 1 < wk.n) next = load_stat(i + 1);
+      }
+      const int sb = i % C::kNS;
+      if (!mbar_wait(&s_full[sb], (i / C::kNS) & 1, abort, kWaitNs)) {
+        give_up();
+        ok = false;
+      }
+      // (an expired wait: every thread still walks the block barriers)
+      // columns [lo, hi) or, for query rows, below sk are seen by this row
+      int lo, hi, sk = 0;
+      bool all;
+      if (kKeys) {
+        lo = r - off - t0;
+        hi = p.window > 0 && r >= p.sinks ? min(nq - t0, lo + p.window) : nq - t0;
+        all = t0 + kBN <= nq && t0 + off >= wk.r0 + kBM - 1 &&
+              (p.window == 0 || wk.r0 + kBM <= p.sinks || t0 + kBN - 1 + off < wk.r0 + p.window);
+      } else {
+        hi = min(r + off, nk - 1) + 1 - t0;
+        lo = p.window > 0 ? r + off - p.window + 1 - t0 : 0;
+        sk = p.sinks - t0;
+        all = t0 + kBN - 1 <= min(wk.r0 + off, nk - 1) &&
+              (p.window == 0 || t0 > wk.r0 + kBM - 1 + off - p.window || t0 + kBN <= p.sinks);
+      }
+      const float *ls = stat + (i & 1) * 2 * kBN + g * kHalf;
+      const uint32_t ts = tmem + lanes + C::kTS + sb * kBN + g * kHalf;
+      float v[kHalf];
+      if (ok) {
+        tc_fence_after();
+        const unsigned long long cc = pair(prm.c, prm.c);
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32) tmem_ld32(ts + c, *reinterpret_cast<float (*)[32]>(v + c));
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32) tmem_wait_ld32(*reinterpret_cast<float (*)[32]>(v + c));
+        if (kFirst && !kSecond) {                          // the scores may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[0]);
+        }
+        const unsigned long long mm = pair(-row_lse, -row_lse);
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 4) {
+          unsigned long long m0 = mm, m1 = mm;
+          if (kKeys) {
+            const float4 x = *reinterpret_cast<const float4 *>(ls + c);
+            m0 = pair(-x.x, -x.y);
+            m1 = pair(-x.z, -x.w);
+          }
+          unpair(fma2(pair(v[c], v[c + 1]), cc, m0), v[c], v[c + 1]);
+          unpair(fma2(pair(v[c + 2], v[c + 3]), cc, m1), v[c + 2], v[c + 3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[c + e] = ex2(v[c + e]);
+        }
+        if (!all) {
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) {
+            const int j = g * kHalf + c;
+            if (!(j < hi && (j >= lo || j < sk))) v[c] = 0.0f;
+          }
+        }
+        // walked rows that nobody sees, zeroed before a product reads them
+        bool dead = false;
+        if (kKeys)
+          dead = t0 + kBN > nq && nq < p.T;
+        else
+          dead = dead_keys(p, nk).any(t0, kBN);
+        if (dead) {
+          if (kFirst && kSecond && !mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
+            give_up();
+            ok = false;
+          }
+          if (!kFirst && !mbar_wait(&w_full[i % C::kNW], (i / C::kNW) & 1, abort, kWaitNs)) {
+            give_up();
+            ok = false;
+          }
+          const bool mine = tid < kBN && (kKeys ? t0 + tid >= nq : dead_keys(p, nk).in(t0 + tid));
+          if (ok && mine)
+            for (int c = 0; c < DH / 64; ++c)
+              for (int e = 0; e < 8; ++e) {
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                const int o = c * (kBN * 128) + tid * 128 + e * 16;
+                if (kFirst) *reinterpret_cast<uint4 *>(sm + C::kOffU + (i & 1) * C::kTile + o) = z;
+                if (kSecond) *reinterpret_cast<uint4 *>(sm + C::kOffW + (i % C::kNW) * C::kTile + o) = z;
+              }
+          fence_proxy_async_smem();
+        }
+        if (kSecond) {
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = bf16x2(v[c + 2 * e], v[c + 2 * e + 1]);
+            tmem_st16u(ts + c / 2, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[sb]);
+        }
+      }
+      if (kFirst && ok) {
+        if (!mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
+          give_up();
+          ok = false;
+        } else {
+          tc_fence_after();
+          const uint32_t td = tmem + lanes + C::kTdP + g * kHalf;
+          const unsigned long long dd = pair(-row_delta, -row_delta);
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            float d[32];
+            tmem_ld32(td + c, d);
+            tmem_wait_ld32(d);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              unsigned long long d0 = dd, d1 = dd;
+              if (kKeys) {
+                const float4 x = *reinterpret_cast<const float4 *>(ls + kBN + c + e);
+                d0 = pair(-x.x, -x.y);
+                d1 = pair(-x.z, -x.w);
+              }
+              float a, bb;
+              unpair(mul2(add2(pair(d[e], d[e + 1]), d0), pair(v[c + e], v[c + e + 1])), a, bb);
+              if (!all) {                                  // hidden: 0, whatever dP holds
+                if (v[c + e] == 0.0f) a = 0.0f;
+                if (v[c + e + 1] == 0.0f) bb = 0.0f;
+              }
+              w[e / 2] = bf16x2(a, bb);
+              unpair(mul2(add2(pair(d[e + 2], d[e + 3]), d1), pair(v[c + e + 2], v[c + e + 3])), a, bb);
+              if (!all) {
+                if (v[c + e + 2] == 0.0f) a = 0.0f;
+                if (v[c + e + 3] == 0.0f) bb = 0.0f;
+              }
+              w[e / 2 + 1] = bf16x2(a, bb);
+            }
+            tmem_st16u(td + c / 2, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ds_full);
+        }
+      }
+      if (kKeys && i + 1 < wk.n) store_stat(i + 1, next);
+      if (!kKeys && !ok) break;
+    }
+    if (ok && !mbar_wait(done, 0, abort, kWaitNs)) {
+      give_up();
+      ok = false;
+    }
+    if (ok) {
+      tc_fence_after();
+      const bool live = r < (kKeys ? nk : nq);
+      constexpr int kCols = DH / 2;                        // of this warp group
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {               // first, second
+        if (part == 0 ? !kFirst : !kSecond) continue;
+        const uint32_t t = tmem + lanes + (part == 0 ? 0 : C::kTSecond) + g * kCols;
+        const float f = part == 0 ? p.scale : 1.0f;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(part == 1 ? p.dv : kKeys ? p.dk : p.dq);
+        dst += kKeys ? ((static_cast<long long>(wk.b) * p.S + r) * p.Hkv + wk.kvh) * DH
+                     : ((static_cast<long long>(wk.b) * p.T + r) * p.Hq + wk.h) * DH;
+        float *part_dst = prm.parts + slot + static_cast<size_t>(part * kBM + row) * DH;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 32) {
+          float o[32];
+          if (wk.n > 0) {
+            tmem_ld32(t + c, o);
+            tmem_wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          }
+          if (!live) continue;
+          if (whole_tile) {
+            store_row32(dst + g * kCols + c, o, f, prm.v8 != 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(part_dst + g * kCols + c + e) =
+                  make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap q_rows, const __grid_constant__ CUtensorMap do_rows,
+                   const __grid_constant__ CUtensorMap k_rows, const __grid_constant__ CUtensorMap v_rows,
+                   const __grid_constant__ CUtensorMap q_tile, const __grid_constant__ CUtensorMap do_tile,
+                   const __grid_constant__ CUtensorMap k_tile, const __grid_constant__ CUtensorMap v_tile,
+                   const __grid_constant__ Params prm) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const AttnArgs &p = prm.a;
+  if ((smem_u32(sm) & 1023u) != 0u) {
+    if (threadIdx.x == 0 && p.dev_status) atomicCAS(p.dev_status, 0, RGLRU_ERR_UNSUPPORTED);
+    return;
+  }
+  constexpr int kBN = DH == 256 ? 64 : 128;
+  constexpr unsigned kKinds = DH == 256 ? 2 : 1;
+  const int off = p.S - p.T, G = p.Hq / p.Hkv;
+  Walk w = {};
+  if (blockIdx.x < kKinds * prm.n_kv) {
+    const bool second = blockIdx.x >= prm.n_kv;            // 256 wide: dK blocks, then dV blocks
+    const unsigned x = second ? blockIdx.x - prm.n_kv : blockIdx.x;
+    const unsigned heads = static_cast<unsigned>(p.B) * p.Hkv;
+    const int bk = static_cast<int>(x % heads);
+    w.b = bk / p.Hkv;
+    w.kvh = bk % p.Hkv;
+    w.len = row_lens(p, w.b);
+    const PieceAt at = piece_at(prm.pl, static_cast<int>(x / heads));
+    w.r0 = at.tile * kBM;
+    if (w.r0 >= w.len.nk) return;
+    w.st = steps_of(query_range(w.r0, kBM, w.len.nq, w.len.nk, off, p.window, p.sinks), kBN, G);
+    w.first = at.piece * prm.pl.len;
+    const int last = min(w.first + prm.pl.len, w.st.n);
+    if (w.first >= last && at.piece > 0) return;
+    w.n = max(last - w.first, 0);
+    const bool whole = w.st.n <= prm.pl.len;
+    const size_t slot =
+        (static_cast<size_t>(bk) * prm.pl.slots + first_slot(prm.pl, at.tile) + at.piece) * 2 * kBM * DH;
+    if (w.n == 0) {                                        // seen by no query: zero gradients
+      const int rows = min(kBM, w.len.nk - w.r0);
+      for (int part = 0; part < 2; ++part) {
+        if (DH == 256 && (part == 1) != second) continue;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(part == 1 ? p.dv : p.dk);
+        for (int i = threadIdx.x; i < rows * (DH / 8); i += kThreads)
+          reinterpret_cast<uint4 *>(
+              dst + ((static_cast<long long>(w.b) * p.S + w.r0 + i / (DH / 8)) * p.Hkv + w.kvh) * DH)[i % (DH / 8)] =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      return;
+    }
+    if constexpr (DH == 256) {
+      if (second)
+        walk<DH, true, false, true>(prm, &k_rows, &v_rows, &q_tile, &do_tile, w, whole, slot, sm);
+      else
+        walk<DH, true, true, false>(prm, &k_rows, &v_rows, &q_tile, &do_tile, w, whole, slot, sm);
+    } else {
+      walk<DH, true, true, true>(prm, &k_rows, &v_rows, &q_tile, &do_tile, w, whole, slot, sm);
+    }
+    return;
+  }
+  unsigned x = blockIdx.x - kKinds * prm.n_kv;
+  w.h = static_cast<int>(x % static_cast<unsigned>(p.Hq));
+  x /= static_cast<unsigned>(p.Hq);
+  w.b = static_cast<int>(x % static_cast<unsigned>(p.B));
+  w.kvh = w.h / G;
+  w.r0 = (prm.n_qt - 1 - static_cast<int>(x / static_cast<unsigned>(p.B))) * kBM;
+  w.len = row_lens(p, w.b);
+  if (w.r0 >= w.len.nq) return;
+  const int last = min(w.r0 + kBM, w.len.nq) - 1;
+  w.kt = key_tiles(w.r0 + off, last + off, w.len.nk, p.window, p.sinks, kBN);
+  w.n = w.kt.n;
+  if (w.n == 0) {                                          // sees no key: zero gradients
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.dq);
+    for (int i = threadIdx.x; i < (last - w.r0 + 1) * (DH / 8); i += kThreads)
+      reinterpret_cast<uint4 *>(
+          dst + ((static_cast<long long>(w.b) * p.T + w.r0 + i / (DH / 8)) * p.Hq + w.h) * DH)[i % (DH / 8)] =
+          make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  walk<DH, false, true, false>(prm, &q_rows, &do_rows, &k_tile, &v_tile, w, true, 0, sm);
+}
+
+PiecePlan plan_of(const AttnArgs &p) {
+  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, kBM, p.dh == 256 ? 64 : 128, 2 * 148);
+}
+
+template <int DH>
+cudaError_t launch(const AttnArgs &p, const PiecePlan &pl, const float *delta, float *parts, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = opt_in_smem(attn_bwd_tc_kernel<DH>, smem_bytes<DH>(), done);
+  if (e != cudaSuccess) return e;
+  constexpr int kBN = DH == 256 ? 64 : 128;
+  const Strided dout = {p.dout, static_cast<long long>(p.T) * p.Hq * DH, static_cast<long long>(p.Hq) * DH, DH};
+  CUtensorMap m[8];
+  const bool ok = attn_map(&m[0], p.q, p.B, p.T, p.Hq, DH, kBM) && attn_map(&m[1], dout, p.B, p.T, p.Hq, DH, kBM) &&
+                  attn_map(&m[2], p.k, p.B, p.S, p.Hkv, DH, kBM) && attn_map(&m[3], p.v, p.B, p.S, p.Hkv, DH, kBM) &&
+                  attn_map(&m[4], p.q, p.B, p.T, p.Hq, DH, kBN) && attn_map(&m[5], dout, p.B, p.T, p.Hq, DH, kBN) &&
+                  attn_map(&m[6], p.k, p.B, p.S, p.Hkv, DH, kBN) && attn_map(&m[7], p.v, p.B, p.S, p.Hkv, DH, kBN);
+  if (!ok) return cudaErrorInvalidValue;
+  Params prm;
+  prm.a = p;
+  prm.pl = pl;
+  prm.delta = delta;
+  prm.parts = parts;
+  prm.n_qt = ceil_div(p.T, kBM);
+  prm.n_kv = static_cast<unsigned>(static_cast<long long>(pl.slots) * p.B * p.Hkv);
+  const uintptr_t outs = reinterpret_cast<uintptr_t>(p.dq) | reinterpret_cast<uintptr_t>(p.dk) |
+                         reinterpret_cast<uintptr_t>(p.dv);
+  prm.v8 = (outs & 31u) == 0 ? 1 : 0;
+  prm.c = p.scale * kLog2e;
+  const unsigned grid = (DH == 256 ? 2u : 1u) * prm.n_kv +
+                        static_cast<unsigned>(static_cast<long long>(prm.n_qt) * p.B * p.Hq);
+  attn_bwd_tc_kernel<DH><<<grid, kThreads, smem_bytes<DH>(), st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_bwd_tc_workspace_bytes(const AttnArgs &p) {
+  return attn_delta_bytes(p) + attn_parts_bytes(p, plan_of(p));
+}
+
+cudaError_t launch_attn_bwd_tc(const AttnArgs &p, void *ws, cudaStream_t st) {
+  const PiecePlan pl = plan_of(p);
+  float *delta = static_cast<float *>(ws);
+  float *parts = delta + attn_delta_bytes(p) / sizeof(float);
+  cudaError_t e = launch_attn_delta(p, RGLRU_IO_BF16, delta, st);
+  if (e != cudaSuccess) return e;
+  switch (p.dh) {
+    case 64: e = launch<64>(p, pl, delta, parts, st); break;
+    case 128: e = launch<128>(p, pl, delta, parts, st); break;
+    default: e = launch<256>(p, pl, delta, parts, st); break;
+  }
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(p, RGLRU_IO_BF16, pl, parts, st);
+}
+
+}  // namespace rglru
