@@ -107,8 +107,6 @@ template <bool kKeys, int kBN> __device__ __forceinline__ void step_at(const Wal
   }
 }
 
-__device__ __forceinline__ void bar_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 template <int DH, bool kKeys, bool kFirst, bool kSecond>
 __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, const CUtensorMap *my,
                                      const CUtensorMap *mu, const CUtensorMap *mw, const Walk &wk,
@@ -116,7 +114,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
   using C = Cfg<DH, kFirst, kSecond>;
   constexpr int kBN = C::kBN, kHalf = kBN / 2;
   const AttnArgs &p = prm.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int G = p.Hq / p.Hkv, off = p.S - p.T;
   uint64_t *x_full = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
   uint64_t *u_full = x_full + 1, *u_empty = u_full + 2;
@@ -201,78 +199,88 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
     }
   } else if (warp == 9) {
     // ============================= MMA issuer =============================
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t id_o = idesc_bf16_f32(kBM, DH, false, true);
-      bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
-          give_up();
-          ok = false;
-        }
-        if (ok) tc_fence_after();
-        return ok;
-      };
-      // rows (K-major, resident) times tile (K-major): D = R T^T over DH
-      auto scores = [&](uint32_t d, int off_rows, int off_tile) {
-        const uint64_t ad = sdesc_sw128(smem_u32(sm + off_rows), 16, 1024);
-        const uint64_t bd = sdesc_sw128(smem_u32(sm + off_tile), 16, 1024);
+    // The whole warp walks, one elected lane issues.
+    constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
+    constexpr uint32_t id_o = idesc_bf16_f32(kBM, DH, false, true);
+    const uint32_t base = smem_u32(sm);
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
+        give_up();
+        ok = false;
+      }
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    // (one lane) rows (K-major, resident) times tile (K-major): D = R T^T over DH
+    auto scores = [&](uint32_t d, uint32_t rows, uint32_t tile) {
+      const uint32_t ad = desc_lo(base + rows, 16), bd = desc_lo(base + tile, 16);
 #pragma unroll
-        for (int k = 0; k < DH / 16; ++k)
-          mma_bf16(d, ad + static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * (kBM * 128)) >> 4),
-                   bd + static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4), id_s,
-                   k > 0 ? 1u : 0u);
-      };
-      // weights in TMEM (each half of the columns at the start of its scores)
-      // times tile (MN-major): D += A T
-      auto product = [&](uint32_t d, uint32_t a, int off_tile, bool add) {
-        const uint64_t bd = sdesc_sw128(smem_u32(sm + off_tile), kBN * 128, 1024);
+      for (int k = 0; k < DH / 16; ++k)
+        mma_ss(d, ad + (((k & 3) * 32 + (k >> 2) * (kBM * 128)) >> 4),
+               bd + (((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4), id_s, k > 0 ? 1u : 0u);
+    };
+    // (one lane) weights in TMEM (each half of the columns at the start of its
+    // scores) times tile (MN-major): D += A T
+    auto product = [&](uint32_t d, uint32_t a, uint32_t tile, bool add) {
+      const uint32_t bd = desc_lo(base + tile, kBN * 128);
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          mma_bf16_ts(d, a + (k / (kHalf / 16)) * kHalf + (k % (kHalf / 16)) * 8,
-                      bd + static_cast<uint64_t>((k * 16 * 128) >> 4), id_o, (add || k > 0) ? 1u : 0u);
-      };
-      auto u_at = [&](int i) { return C::kOffU + (i & 1) * C::kTile; };
-      auto w_at = [&](int i) { return C::kOffW + (i % C::kNW) * C::kTile; };
-      auto issue_s = [&](int i) {
-        if (!wait(&u_full[i & 1], (i >> 1) & 1)) return;
+      for (int k = 0; k < kBN / 16; ++k)
+        mma_ts(d, a + (k / (kHalf / 16)) * kHalf + (k % (kHalf / 16)) * 8, bd + ((k * 16 * 128) >> 4),
+               id_o, k > 0 ? 1u : add);
+    };
+    auto u_at = [&](int i) { return static_cast<uint32_t>(C::kOffU + (i & 1) * C::kTile); };
+    auto w_at = [&](int i) { return static_cast<uint32_t>(C::kOffW + (i % C::kNW) * C::kTile); };
+    auto issue_s = [&](int i) {
+      if (!wait(&u_full[i & 1], (i >> 1) & 1)) return;
+      if (elect_one()) {
         scores(tmem + C::kTS + (i % C::kNS) * kBN, 0, u_at(i));
         mma_commit(&s_full[i % C::kNS]);
         if (!kFirst) mma_commit(&u_empty[i & 1]);
-      };
-      auto issue_dp = [&](int i) {
-        if (!wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+      }
+      __syncwarp();
+    };
+    auto issue_dp = [&](int i) {
+      if (!wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+      if (elect_one()) {
         scores(tmem + C::kTdP, C::kOffY, w_at(i));
         mma_commit(dp_full);
         if (!kSecond) mma_commit(&w_empty[i % C::kNW]);
-      };
-      auto issue_second = [&](int i) {
-        if (!kFirst && !wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+      }
+      __syncwarp();
+    };
+    auto issue_second = [&](int i) {
+      if (!kFirst && !wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) return;
+      if (elect_one()) {
         product(tmem + C::kTSecond, tmem + C::kTS + (i % C::kNS) * kBN, w_at(i), i > 0);
         mma_commit(&w_empty[i % C::kNW]);
-      };
-      wait(x_full, 0);
-      if (ok) issue_s(0);
-      if (kFirst && ok) issue_dp(0);
-      for (int i = 0; i < wk.n && ok; ++i) {
-        if (!kFirst) {
-          if (i + 1 < wk.n) issue_s(i + 1);
-          if (ok && wait(&p_full[i & 1], (i >> 1) & 1)) issue_second(i);
-          continue;
-        }
-        // P is in place, or S was read: the score columns are free after `second`
-        if (!wait(&p_full[0], i & 1)) break;
-        if (kSecond) issue_second(i);
-        if (ok && i + 1 < wk.n) issue_s(i + 1);
-        if (ok && wait(ds_full, i & 1)) {
+      }
+      __syncwarp();
+    };
+    wait(x_full, 0);
+    if (ok) issue_s(0);
+    if (kFirst && ok) issue_dp(0);
+    for (int i = 0; i < wk.n && ok; ++i) {
+      if (!kFirst) {
+        if (i + 1 < wk.n) issue_s(i + 1);
+        if (wait(&p_full[i & 1], (i >> 1) & 1)) issue_second(i);
+        continue;
+      }
+      // P is in place, or S was read: the score columns are free after `second`
+      if (!wait(&p_full[0], i & 1)) break;
+      if (kSecond) issue_second(i);
+      if (ok && i + 1 < wk.n) issue_s(i + 1);
+      if (wait(ds_full, i & 1)) {
+        if (elect_one()) {
           product(tmem, tmem + C::kTdP, u_at(i), i > 0);
           mma_commit(&u_empty[i & 1]);
-          if (i + 1 < wk.n) issue_dp(i + 1);
         }
+        __syncwarp();
+        if (i + 1 < wk.n) issue_dp(i + 1);
       }
-      mma_commit(done);
-      if (*abort) mbar_wait_drain(done, 0, kDrainNs);
     }
+    if (elect_one()) mma_commit(done);
+    if (*abort) mbar_wait_drain(done, 0, kDrainNs);
   } else {
     // =============================== weights ==============================
     const int g = warp >> 2, row = (warp & 3) * 32 + lane;

@@ -5,12 +5,13 @@
 //   l = l 2^(m - m') + sum p,  O = O 2^(m - m') + P V,  out = O / l
 //
 // One block takes 128 queries of one head and walks the key tiles that its mask
-// leaves. Warps 0-3 are the softmax: thread = query row = TMEM lane, a row's 128
-// scores in registers, so its maximum and sum need no shuffles. Warp 4 issues
-// the TMA copies (K and V through one ring of slots, 128 keys x up to 128
-// columns each, in the order of use), warp 5 the MMAs: S from shared memory
-// (Q and K both K-major), P V with P as the TMEM operand (bf16, written over
-// the scores it came from) and V MN-major as TMA left it. The accumulator O
+// leaves. Warps 0-7 are the softmax, thread = query row = TMEM lane, warp group
+// g the columns 64 g ..: a row's maximum is one exchange through shared memory
+// between two threads. Warp 8 issues the TMA copies (K and V through one ring of
+// slots, 128 keys x up to 128 columns each, in the order of use), warp 9 the
+// MMAs: S from shared memory (Q and K both K-major), P V with P as the TMEM
+// operand (bf16, written over the scores it came from) and V MN-major as TMA
+// left it. The accumulator O
 // stays in TMEM for the whole walk; the reference maximum m moves only when it
 // is 8 or more behind in log2 units (weights up to 2^8 keep their relative
 // precision), so O is seldom rescaled.
@@ -31,7 +32,7 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSite = 7;
@@ -50,8 +51,10 @@ template <int DH> struct Cfg {
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
   static constexpr int kNumBars = 2 * kSlots + 1 + 2 * kNS + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 16;
+  static constexpr int kOffMax = kOffMisc + 16;            // [2][2 groups][128 rows]
+  static constexpr int kSmem = kOffMax + 2 * 2 * kBM * 4;
   static constexpr int kBlocks = DH == 256 ? 1 : 2;      // per SM
+  static constexpr bool kReread = kBlocks == 2;
 };
 static_assert(Cfg<256>::kSmem <= kMaxSmem && 2 * (Cfg<128>::kSmem + 1024) <= 233472, "shared memory");
 
@@ -84,7 +87,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const int off = p.S - p.T, kvh = h / (p.Hq / p.Hkv);
   const int q_last = min(q0 + kBM, n.nq) - 1;
   const KeyTiles kt = key_tiles(q0 + off, q_last + off, n.nk, p.window, p.sinks, kBN);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
   if (kt.n == 0) {                                       // no query of the tile sees a key
     for (int i = tid; i < (q_last - q0 + 1) * (DH / 8); i += kThreads) {
@@ -104,7 +107,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   uint64_t *s_full = q_full + 1;
   uint64_t *p_full = s_full + C::kNS;
   uint64_t *o_done = p_full + C::kNS;
-  uint64_t *drained = o_done + 1;                        // used when a wait expired
+  uint64_t *all_done = o_done + 1;                       // every MMA of the block
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + C::kOffMisc + 4);
   if (tid == 0) {
@@ -115,14 +118,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     mbar_init(q_full, 1);
     for (int s = 0; s < C::kNS; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[s], 8);
     }
     mbar_init(o_done, 1);
-    mbar_init(drained, 1);
+    mbar_init(all_done, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
   }
@@ -147,7 +150,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     return (i + 1 < kt.n ? 2 * i + 2 : 2 * i + 1) * C::kPer;
   };
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ============================ TMA producer ============================
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, C::kQBytes);
@@ -189,84 +192,91 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           mbar_wait_drain(&full[j % C::kSlots], (j / C::kSlots) & 1, kDrainNs);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ============================= MMA issuer =============================
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
-      bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
-          give_up();
-          ok = false;
-        }
-        return ok;
-      };
-      auto scores = [&](int i) {
-        const int f0 = at(i, false);
-        for (int x = 0; x < C::kPer; ++x) {
-          const int s = (f0 + x) % C::kSlots;
-          if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
-          tc_fence_after();
-          const uint64_t ad = sdesc_sw128(smem_u32(sm) + x * (C::kCols / 64) * (kBM * 128), 16, 1024);
-          const uint64_t bd = sdesc_sw128(smem_u32(sm + C::kOffRing + s * C::kSlotBytes), 16, 1024);
+    // The whole warp walks, one elected lane issues.
+    constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
+    constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
+    const uint32_t base = smem_u32(sm);
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
+        give_up();
+        ok = false;
+      }
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    auto scores = [&](int i) {
+      const int f0 = at(i, false);
+      const uint32_t d = t_s + (i % C::kNS) * kBN;
+      for (int x = 0; x < C::kPer; ++x) {
+        const int s = (f0 + x) % C::kSlots;
+        if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
+        const uint32_t ad = desc_lo(base + x * (C::kCols / 64) * (kBM * 128), 16);
+        const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, 16);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < C::kCols / 16; ++k) {
             // a K step of 16 moves 32 bytes along the 128-byte row; 64-column
             // blocks lie 128 rows x 128 bytes apart
-            const uint64_t o = static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4);
-            mma_bf16(t_s + (i % C::kNS) * kBN, ad + o, bd + o, id_s, (x > 0 || k > 0) ? 1u : 0u);
+            const uint32_t o = ((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4;
+            mma_ss(d, ad + o, bd + o, id_s, k > 0 ? 1u : x > 0);
           }
           mma_commit(&empty[s]);
+          if (x == C::kPer - 1) mma_commit(&s_full[i % C::kNS]);
         }
-        mma_commit(&s_full[i % C::kNS]);
-      };
-      auto values = [&](int i) {
-        if (!wait(&p_full[i % C::kNS], (i / C::kNS) & 1)) return;
-        const int f0 = at(i, true);
-        for (int x = 0; x < C::kPer; ++x) {
-          const int s = (f0 + x) % C::kSlots;
-          if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
-          tc_fence_after();
-          const uint64_t bd = sdesc_sw128(smem_u32(sm + C::kOffRing + s * C::kSlotBytes), kBN * 128, 1024);
+        __syncwarp();
+      }
+    };
+    auto values = [&](int i) {
+      if (!wait(&p_full[i % C::kNS], (i / C::kNS) & 1)) return;
+      const int f0 = at(i, true);
+      const uint32_t a = t_s + (i % C::kNS) * kBN;
+      for (int x = 0; x < C::kPer; ++x) {
+        const int s = (f0 + x) % C::kSlots;
+        if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
+        const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBN / 16; ++k)
-            mma_bf16_ts(t_o + x * C::kCols, t_s + (i % C::kNS) * kBN + k * 8,
-                        bd + static_cast<uint64_t>((k * 16 * 128) >> 4), id_o,
-                        (i > 0 || k > 0) ? 1u : 0u);
+            mma_ts(t_o + x * C::kCols, a + (k >> 2) * 64 + (k & 3) * 8, bd + ((k * 16 * 128) >> 4), id_o, k > 0 ? 1u : i > 0);
           mma_commit(&empty[s]);
+          if (x == C::kPer - 1) mma_commit(o_done);
         }
-        mma_commit(o_done);
-      };
-      wait(q_full, 0);
-      if (ok) scores(0);
-      for (int i = 0; i < kt.n && ok; ++i) {
-        if (C::kNS == 2 && i + 1 < kt.n) scores(i + 1);
-        if (ok) values(i);
-        if (C::kNS == 1 && ok && i + 1 < kt.n) scores(i + 1);
+        __syncwarp();
       }
-      if (*abort) {
-        mma_commit(drained);
-        mbar_wait_drain(drained, 0, kDrainNs);
-      }
+    };
+    wait(q_full, 0);
+    if (ok) scores(0);
+    for (int i = 0; i < kt.n && ok; ++i) {
+      if (C::kNS == 2 && i + 1 < kt.n) scores(i + 1);
+      if (ok) values(i);
+      if (C::kNS == 1 && ok && i + 1 < kt.n) scores(i + 1);
     }
+    if (elect_one()) mma_commit(all_done);
+    if (*abort) mbar_wait_drain(all_done, 0, kDrainNs);
   } else {
     // =============================== softmax ==============================
-    const int row = warp * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // Warp group g: columns 64 g .. of a tile. Thread = row = TMEM lane.
+    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int pos = q0 + row + off;
     const DeadKeys dead = dead_keys(p, n.nk);
+    float *shared_max = reinterpret_cast<float *>(sm + C::kOffMax);
     float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int i = 0; i < kt.n; ++i) {
-      const int s = i % C::kNS, k0 = kt.tile(i) * kBN;
-      if (!mbar_wait(&s_full[s], (i / C::kNS) & 1, abort, kWaitNs)) {
+    bool ok = true;                  // a warp whose wait expired still meets the block barriers
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
         give_up();
         ok = false;
-        break;
       }
-      tc_fence_after();
-      const uint32_t ts = t_s + s * kBN + lanes;
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    for (int i = 0; i < kt.n; ++i) {
+      const int s = i % C::kNS, k0 = kt.tile(i) * kBN;
+      const uint32_t ts = t_s + s * kBN + g * 64 + lanes;
       // whether every query of the tile sees every key of the tile
       const bool whole = k0 + kBN - 1 <= min(q0 + off, n.nk - 1) &&
                          (p.window == 0 || k0 > q0 + kBM - 1 + off - p.window || k0 + kBN <= p.sinks);
@@ -276,97 +286,96 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (whole) return;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const int j = c * 32 + e;
+          const int j = g * 64 + c * 32 + e;
           if (!(j <= hi && (j >= lo || j < sk))) v[e] = -INFINITY;
         }
       };
-      // the scores are read twice, for the maximum and for the weights: a second
-      // read of TMEM costs less than 128 registers a thread
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        float v[2][32];
-        tmem_ld32(ts + c * 32, v[0]);
-        tmem_ld32(ts + c * 32 + 32, v[1]);
-        tmem_wait_ld32(v[0]);
-        tmem_wait_ld32(v[1]);
+      float v[2][32], mx[2] = {-INFINITY, -INFINITY};
+      if (wait(&s_full[s], (i / C::kNS) & 1)) {
+        // two blocks an SM leave a thread under 102 registers: the scores are read
+        // 32 at a time, once for the maximum and once for the weights
+        if constexpr (!C::kReread) {
+          tmem_ld32(ts, v[0]);
+          tmem_ld32(ts + 32, v[1]);
+          tmem_wait_ld32(v[0]);
+          tmem_wait_ld32(v[1]);
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          mask(v[x], c + x);
+          float(&u)[32] = v[C::kReread ? 0 : x];
+          if constexpr (C::kReread) {
+            tmem_ld32(ts + x * 32, u);
+            tmem_wait_ld32(u);
+          }
+          mask(u, x);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) mx[x] = max3(mx[x], v[x][e], v[x][e + 1]);
+          for (int e = 0; e < 32; e += 2) mx[x] = max3(mx[x], u[e], u[e + 1]);
         }
       }
-      const float top = fmaxf(mx[0], mx[1]) * prm.c;
+      const float mine = fmaxf(mx[0], mx[1]);
+      shared_max[((i & 1) * 2 + g) * kBM + row] = mine;
+      bar_sync_softmax();
+      if (!ok) continue;
+      const float top = fmaxf(mine, shared_max[((i & 1) * 2 + (g ^ 1)) * kBM + row]) * prm.c;
       const bool grow = top > m + kSlack || m == -INFINITY;
       const float mn = grow ? fmaxf(top, m) : m;
-      if (__any_sync(0xFFFFFFFFu, grow && mn != m)) {
+      if (__any_sync(0xFFFFFFFFu, mn != m)) {
         const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
         l *= f;
         m = mn;
-        if (i > 0) {                                     // O so far: P V of the last tile is done
-          if (!mbar_wait(o_done, (i - 1) & 1, abort, kWaitNs)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (i > 0 && wait(o_done, (i - 1) & 1)) {        // O so far: P V of the last tile is done
 #pragma unroll 1
-          for (int c = 0; c < DH / 32; ++c) {
+          for (int c = 0; c < DH / 64; ++c) {
+            const uint32_t to = t_o + lanes + g * (DH / 2) + c * 32;
             float o[32];
-            tmem_ld32(t_o + lanes + c * 32, o);
+            tmem_ld32(to, o);
             tmem_wait_ld32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(t_o + lanes + c * 32, o);
+            tmem_st32(to, o);
           }
           tmem_wait_st();
         }
+        if (!ok) continue;
       }
       const float base = m == -INFINITY ? 0.0f : m;
       const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-base, -base);
-      unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
-      // the weights of columns 32 c .. go to TMEM columns 16 c ..: over scores
-      // that were read already
-      float v[2][32];
-      tmem_ld32(ts, v[0]);
-      tmem_wait_ld32(v[0]);
+      unsigned long long sum[2] = {0ull, 0ull};
+      // the weights of this group's columns go to the first half of its score columns
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c < 3) tmem_ld32(ts + c * 32 + 32, v[(c + 1) & 1]);
-        mask(v[c & 1], c);
+      for (int c = 0; c < 2; ++c) {
+        float(&u)[32] = v[C::kReread ? 0 : c];
+        if constexpr (C::kReread) {
+          tmem_ld32(ts + c * 32, u);
+          tmem_wait_ld32(u);
+          mask(u, c);
+        }
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float a, bb;
-          unpair(fma2(pair(v[c & 1][e], v[c & 1][e + 1]), cc, mm), a, bb);
+          unpair(fma2(pair(u[e], u[e + 1]), cc, mm), a, bb);
           a = ex2(a);
           bb = ex2(bb);
-          sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pair(a, bb));
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, bb));
           w[e / 2] = bf16x2(a, bb);
         }
-        if (c < 3) tmem_wait_ld32(v[(c + 1) & 1]);
         tmem_st16u(ts + c * 16, w);
       }
       float s0, s1;
-      unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+      unpair(add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
       if (dead.any(k0, kBN)) {
         // zero the value rows that no query sees, once V is there
         const int f0 = at(i, true);
-        for (int x = 0; x < C::kPer && ok; ++x) {
+        for (int x = 0; x < C::kPer; ++x) {
           const int sl = (f0 + x) % C::kSlots;
-          if (!mbar_wait(&full[sl], ((f0 + x) / C::kSlots) & 1, abort, kWaitNs)) {
-            give_up();
-            ok = false;
-          } else if (dead.in(k0 + row)) {
+          if (wait(&full[sl], ((f0 + x) / C::kSlots) & 1) && g == 0 && dead.in(k0 + row))
             for (int c = 0; c < C::kCols / 64; ++c)
               for (int e = 0; e < 8; ++e)
                 *reinterpret_cast<uint4 *>(sm + C::kOffRing + sl * C::kSlotBytes + c * (kBN * 128) +
                                            row * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
         }
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         fence_proxy_async_smem();
       }
       tmem_wait_st();
@@ -374,20 +383,19 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[s]);
     }
-    if (ok) {
-      // with two score buffers the product before the last may still run
-      bool done = kt.n < 2 || mbar_wait(o_done, (kt.n - 2) & 1, abort, kWaitNs);
-      done = done && mbar_wait(o_done, (kt.n - 1) & 1, abort, kWaitNs);
-      if (!done) give_up();
-      tc_fence_after();
+    // the row's sum, from both groups
+    shared_max[((kt.n & 1) * 2 + g) * kBM + row] = l;
+    bar_sync_softmax();
+    l += shared_max[((kt.n & 1) * 2 + (g ^ 1)) * kBM + row];
+    if (wait(all_done, 0)) {
       const int t = q0 + row;
-      const bool live = done && t < n.nq;
+      const bool live = t < n.nq;
       const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-      __nv_bfloat16 *dst = out + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * DH;
+      __nv_bfloat16 *dst = out + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * DH + g * (DH / 2);
 #pragma unroll 1
-      for (int c = 0; c < DH / 32; ++c) {
+      for (int c = 0; c < DH / 64; ++c) {
         float o[32];
-        tmem_ld32(t_o + lanes + c * 32, o);
+        tmem_ld32(t_o + lanes + g * (DH / 2) + c * 32, o);
         tmem_wait_ld32(o);
         if (live) {
           if (m == -INFINITY) {
@@ -397,7 +405,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           store_row32(dst + c * 32, o, inv, prm.v8 != 0);
         }
       }
-      if (live && p.lse != nullptr)
+      if (live && g == 0 && p.lse != nullptr)
         p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] =
             m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
     }
@@ -405,7 +413,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, C::kTmem);
+  if (warp == 9) tmem_dealloc(tmem, C::kTmem);
 }
 
 template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
