@@ -11,6 +11,12 @@ __host__ __device__ __forceinline__ bool attn_visible(int j, int pos, int window
   return j <= pos && (window == 0 || j > pos - window || j < sinks);
 }
 
+// A query at `pos` that sees one key: its softmax is constant, so its scores get
+// no gradient, and none is formed (rounding would leave a few units of one).
+__host__ __device__ __forceinline__ bool attn_lone(int pos, int window, int sinks) {
+  return pos == 0 || (window == 1 && sinks == 0);
+}
+
 // Tokens of batch row b: queries and keys (they differ only without lens).
 struct RowLens {
   int nq, nk;

@@ -415,6 +415,11 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           if (lane == 0) mbar_arrive(&p_full[sb]);
         }
       }
+      if (kFirst && !all) {                                // queries that see one key: dS = 0
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c)
+          if (attn_lone(kKeys ? t0 + g * kHalf + c + off : r + off, p.window, p.sinks)) v[c] = 0.0f;
+      }
       if (kFirst && ok) {
         if (!mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
           give_up();

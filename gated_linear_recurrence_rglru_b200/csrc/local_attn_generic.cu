@@ -251,12 +251,13 @@ __device__ __forceinline__ void tile_grads(const AttnArgs &p, const float *qs, c
   for (int i = 0; i < N; ++i) {
     const int r = ty + 16 * i, t = q0 + r;
     const float lse = lses[r], dl = deltas[r];
+    const bool lone = attn_lone(t + off, p.window, p.sinks);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int key = k0 + tx + 16 * j;
       const bool ok = t < n.nq && key < n.nk && attn_visible(key, t + off, p.window, p.sinks);
       w[i][j] = ok ? expf(w[i][j] * p.scale - lse) : 0.0f;
-      ds[i][j] = ok ? w[i][j] * (ds[i][j] - dl) * p.scale : 0.0f;
+      ds[i][j] = ok && !lone ? w[i][j] * (ds[i][j] - dl) * p.scale : 0.0f;
     }
   }
 }

@@ -187,6 +187,8 @@ ATTN_CASES = [  # io, B, T, S, Hq, Hkv, dh, window, sinks, lens, layout
     ("bf16", 1, 20, 1000, 4, 1, 256, 37, 0, None, "dense"),      # keys that no query sees
     ("bf16", 1, 257, 257, 1, 1, 64, 1, 0, None, "dense"),        # every query sees itself alone
     ("f32", 2, 100, 100, 4, 2, 64, 0, 0, None, "slice"),
+    ("f32", 3, 1, 1, 4, 2, 128, 0, 0, None, "dense"), ("f32", 1, 40, 40, 1, 1, 64, 1, 0, None, "dense"),
+    ("bf16", 2, 1, 1, 4, 1, 256, 1024, 4, None, "dense"), ("bf16", 1, 3, 3, 2, 1, 128, 2, 0, None, "dense"),
     ("f32", 1, 70, 200, 2, 1, 128, 60, 3, None, "heads"),
     ("f32", 2, 90, 90, 3, 1, 256, 33, 2, [90, 17], "slice"),
     ("f32", 1, 50, 20, 2, 2, 192, 5, 1, None, "dense"),
@@ -266,6 +268,12 @@ def test_local_attn_bwd(cuda_device, case):
     if lens is not None:
         for b, m in enumerate(lens):
             assert all(torch.all(got[n][b, m:] == 7) for n in grads)
+    # a query that sees one key has a constant softmax: exactly no gradient of its scores
+    pos = np.arange(T) + S - T
+    if lens is None and np.any(pos == 0):
+        assert torch.all(got["dq"][:, int(np.argmax(pos == 0))] == 0)
+    if (window == 1 and sinks == 0) or S == T == 1:
+        assert torch.all(got["dq"] == 0) and torch.all(got["dk"] == 0)
     again = rg.rglru_local_attn_bwd(*args, window=window, sinks=sinks, lens=dl)
     if lens is None:
         assert all(torch.equal(got[n], again[n]) for n in grads)
