@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._abi import LIB, RGLRUError, _io_of, _ptr
+from ._abi import LIB, RGLRUError, _io_of
 
 
 class Strides(ctypes.Structure):
@@ -53,44 +53,76 @@ def _declare(lib):
 _declare(LIB)
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """The call's device, and its stream as the one that allocations belong to."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+class _on:
+    """The call's device, and its stream as the one that allocations belong to; gives the
+    stream's handle. Nothing is switched when both are current already."""
+    __slots__ = ("index", "stream", "held")
+
+    def __init__(self, index, stream):
+        self.index, self.stream, self.held = index, stream, None
+
+    def __enter__(self):
+        current = torch.cuda.current_stream()
+        if self.stream is None and current.device_index == self.index:
+            return current.cuda_stream
+        self.held = contextlib.ExitStack()
+        self.held.enter_context(torch.cuda.device(self.index))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        self.held.enter_context(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.held is not None:
+            self.held.close()
 
 
-def _heads(t, name, like=None):
-    """(B, T, H, dh) of a tensor whose heads are contiguous."""
+def _place(t, name, index):
+    """Refuses what is not a tensor on the call's device (index None: any CUDA device)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _p(t, name, dtype, shape, index, optional=False):
+    """Pointer of a dense tensor on the call's device; dtype or shape None: not looked at."""
+    try:        # the checks below in one expression: what a good call pays for
+        if (t.get_device() == index and (shape is None or t.shape == shape) and t.dtype is dtype
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    _place(t, name, index)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _view(t, name, dtype, shape, index):
+    """Pointer and strides (None: dense) of a (B, T, H, dh) tensor whose heads are contiguous;
+    dtype, shape or index None: any."""
+    _place(t, name, index)
     if t.dim() != 4:
         raise ValueError(f"{name} must be (B, T, heads, dh)")
-    if like is not None and t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.shape
-
-
-def _view(t):
-    """Pointer and strides of a (B, T, H, dh) tensor."""
-    return t.data_ptr(), ctypes.byref(Strides(t.stride(0), t.stride(1), t.stride(2)))
-
-
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-
-
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), Strides(sb, st, sh)
 
 
 def _workspace(workspace, need, dev):
@@ -104,31 +136,63 @@ def _check(st, what):
         raise RGLRUError(st, what)
 
 
+def _sizes(q, k, v=None):
+    """What the shapes of q (B, T, Hq, dh) and k, v (B, S, Hkv, dh) say, and their views."""
+    qv = _view(q, "q", None, None, None)
+    index, dt = q.get_device(), q.dtype
+    io = _io_of(dt)
+    B, T, Hq, dh = q.shape
+    kv = _view(k, "k", dt, None, index)
+    _, S, Hkv, _ = k.shape
+    if k.shape != (B, S, Hkv, dh):
+        raise ValueError(f"k must have shape {(B, S, Hkv, dh)}, got {tuple(k.shape)}")
+    views = (*qv, *kv)
+    if v is not None:
+        views += _view(v, "v", dt, (B, S, Hkv, dh), index)
+    return views, index, dt, io, B, T, S, Hq, Hkv, dh
+
+
+def _same_length(S, T):
+    if S != T:
+        raise ValueError(f"k must have q's {T} tokens, got {S}")
+
+
 def rglru_qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, *, rot=None, base=10000.0,
                            eps=1e-6, q_out=None, k_out=None, stream=None):
     """RMS norm of every head of q (B, T, Hq, dh) and k (B, T, Hkv, dh), and the rotation of
     their first `rot` dims (all of them by default) by their positions (B, T; 0..T-1 by
     default), in one pass. q and k may be slices of a fused projection. Returns (q_out, k_out),
     dense."""
-    B, T, Hq, dh = _heads(q, "q")
-    Hkv = _heads(k, "k", q)[2]
-    _shape(k, "k", (B, T, Hkv, dh))
-    dt, dev = q.dtype, q.device
-    io = _io_of(dt)
-    _same_device(dev, k=k, w_q=w_q, w_k=w_k, positions=positions, q_out=q_out, k_out=k_out)
+    views, dev, dt, io, B, T, S, Hq, Hkv, dh = _sizes(q, k)
+    _same_length(S, T)
     with _on(dev, stream) as st:
         if q_out is None:
-            q_out = torch.empty((B, T, Hq, dh), device=dev, dtype=dt)
+            q_out = torch.empty((B, T, Hq, dh), device=q.device, dtype=dt)
         if k_out is None:
-            k_out = torch.empty((B, T, Hkv, dh), device=dev, dtype=dt)
+            k_out = torch.empty((B, T, Hkv, dh), device=q.device, dtype=dt)
         _check(LIB.rglru_qk_norm_rope_fwd(
-            *_view(q), *_view(k), _ptr(w_q, "w_q", dt, (dh,), optional=True),
-            _ptr(w_k, "w_k", dt, (dh,), optional=True),
-            _ptr(positions, "positions", torch.int32, (B, T), optional=True),
-            _ptr(q_out, "q_out", dt, (B, T, Hq, dh)), _ptr(k_out, "k_out", dt, (B, T, Hkv, dh)),
+            *views, _p(w_q, "w_q", dt, (dh,), dev, True), _p(w_k, "w_k", dt, (dh,), dev, True),
+            _p(positions, "positions", torch.int32, (B, T), dev, True),
+            _p(q_out, "q_out", dt, (B, T, Hq, dh), dev), _p(k_out, "k_out", dt, (B, T, Hkv, dh), dev),
             B, T, Hq, Hkv, dh, dh if rot is None else rot, base, eps, io, st),
             "rglru_qk_norm_rope_fwd")
     return q_out, k_out
+
+
+def _cache(k_cache, v_cache, page_table, dt, B, Hkv, dh, dev):
+    """Pointers and sizes of the caches and the page table."""
+    kc = _p(k_cache, "k_cache", dt, None, dev)
+    if k_cache.dim() != 4:
+        raise ValueError("a cache must be (pages, page_size, Hkv, dh)")
+    pages, page_size = k_cache.shape[:2]
+    if k_cache.shape != (pages, page_size, Hkv, dh):
+        raise ValueError(f"k_cache must have shape {(pages, page_size, Hkv, dh)}, "
+                         f"got {tuple(k_cache.shape)}")
+    vc = _p(v_cache, "v_cache", dt, k_cache.shape, dev)
+    table = _p(page_table, "page_table", torch.int32, None, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must have shape ({B}, max_pages), got {tuple(page_table.shape)}")
+    return kc, vc, table, pages, page_size, page_table.shape[1]
 
 
 def rglru_qk_norm_rope_append(q, k, v, k_cache, v_cache, page_table, positions, w_q=None,
@@ -137,70 +201,47 @@ def rglru_qk_norm_rope_append(q, k, v, k_cache, v_cache, page_table, positions, 
     """The serving form: q normed and rotated into q_out (returned), k normed and rotated and v
     copied into their slots of the paged caches (pages, page_size, Hkv, dh), in place. Position
     p of row b lives in page page_table[b, p // page_size], slot p % page_size. Tokens at
-    negative positions are padding; their rows of q_out are zeros when it is allocated here."""
-    B, T, Hq, dh = _heads(q, "q")
-    Hkv = _heads(k, "k", q)[2]
-    _heads(v, "v", q)
-    _shape(k, "k", (B, T, Hkv, dh))
-    _shape(v, "v", (B, T, Hkv, dh))
-    dt, dev = q.dtype, q.device
-    io = _io_of(dt)
-    _same_device(dev, k=k, v=v, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
-                 positions=positions, w_q=w_q, w_k=w_k, q_out=q_out, dev_status=dev_status)
-    pages, page_size, max_pages = _cache_sizes(k_cache, v_cache, page_table, B, Hkv, dh)
+    negative positions are padding: their rows of q_out are zeros and no slot is written."""
+    views, dev, dt, io, B, T, S, Hq, Hkv, dh = _sizes(q, k, v)
+    _same_length(S, T)
+    kc, vc, table, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, dt, B, Hkv,
+                                                        dh, dev)
     with _on(dev, stream) as st:
         if q_out is None:
-            q_out = torch.zeros((B, T, Hq, dh), device=dev, dtype=dt)
+            q_out = torch.empty((B, T, Hq, dh), device=q.device, dtype=dt)
         _check(LIB.rglru_qk_norm_rope_append(
-            *_view(q), *_view(k), *_view(v), _ptr(w_q, "w_q", dt, (dh,), optional=True),
-            _ptr(w_k, "w_k", dt, (dh,), optional=True),
-            _ptr(positions, "positions", torch.int32, (B, T)),
-            _ptr(q_out, "q_out", dt, (B, T, Hq, dh)), _ptr(k_cache, "k_cache", dt),
-            _ptr(v_cache, "v_cache", dt), _ptr(page_table, "page_table", torch.int32), pages,
-            page_size, max_pages, B, T, Hq, Hkv, dh, dh if rot is None else rot, base, eps, io,
-            _ptr(dev_status, "dev_status", torch.int32, optional=True), st),
+            *views, _p(w_q, "w_q", dt, (dh,), dev, True), _p(w_k, "w_k", dt, (dh,), dev, True),
+            _p(positions, "positions", torch.int32, (B, T), dev),
+            _p(q_out, "q_out", dt, (B, T, Hq, dh), dev), kc, vc, table, pages, page_size,
+            max_pages, B, T, Hq, Hkv, dh, dh if rot is None else rot, base, eps, io,
+            _p(dev_status, "dev_status", torch.int32, None, dev, True), st),
             "rglru_qk_norm_rope_append")
     return q_out
-
-
-def _cache_sizes(k_cache, v_cache, page_table, B, Hkv, dh):
-    if k_cache.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("a cache must be (pages, page_size, Hkv, dh) and page_table (B, max_pages)")
-    pages, page_size = k_cache.shape[:2]
-    _shape(k_cache, "k_cache", (pages, page_size, Hkv, dh))
-    _shape(v_cache, "v_cache", (pages, page_size, Hkv, dh))
-    _shape(page_table, "page_table", (B, page_table.shape[1]))
-    return pages, page_size, page_table.shape[1]
 
 
 def rglru_qk_norm_rope_bwd(q, k, dq_out, dk_out, w_q=None, w_k=None, positions=None, *, rot=None,
                            base=10000.0, eps=1e-6, workspace=None, out=None, stream=None):
     """Backward of rglru_qk_norm_rope_fwd. Returns a dict with dq, dk (dense, the I/O dtype) and
     dw_q, dw_k (fp32). `out` may hold preallocated outputs by name."""
-    B, T, Hq, dh = _heads(q, "q")
-    Hkv = _heads(k, "k", q)[2]
-    _shape(k, "k", (B, T, Hkv, dh))
-    dt, dev, f32 = q.dtype, q.device, torch.float32
-    io = _io_of(dt)
-    g = dict(out or {})
-    _same_device(dev, k=k, dq_out=dq_out, dk_out=dk_out, w_q=w_q, w_k=w_k, positions=positions,
-                 workspace=workspace, **g)
+    views, dev, dt, io, B, T, S, Hq, Hkv, dh = _sizes(q, k)
+    _same_length(S, T)
+    g, f32 = dict(out or {}), torch.float32
     with _on(dev, stream) as st:
         for name, shape, dtype in (("dq", (B, T, Hq, dh), dt), ("dk", (B, T, Hkv, dh), dt),
                                    ("dw_q", (dh,), f32), ("dw_k", (dh,), f32)):
             if g.get(name) is None:
-                g[name] = torch.empty(shape, device=dev, dtype=dtype)
+                g[name] = torch.empty(shape, device=q.device, dtype=dtype)
         need = LIB.rglru_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hkv, dh, io)
-        workspace = _workspace(workspace, need, dev)
+        workspace = _workspace(workspace, need, q.device)
         _check(LIB.rglru_qk_norm_rope_bwd(
-            *_view(q), *_view(k), _ptr(w_q, "w_q", dt, (dh,), optional=True),
-            _ptr(w_k, "w_k", dt, (dh,), optional=True),
-            _ptr(positions, "positions", torch.int32, (B, T), optional=True),
-            _ptr(dq_out, "dq_out", dt, (B, T, Hq, dh)),
-            _ptr(dk_out, "dk_out", dt, (B, T, Hkv, dh)), _ptr(g["dq"], "dq", dt, (B, T, Hq, dh)),
-            _ptr(g["dk"], "dk", dt, (B, T, Hkv, dh)), _ptr(g["dw_q"], "dw_q", f32, (dh,)),
-            _ptr(g["dw_k"], "dw_k", f32, (dh,)), B, T, Hq, Hkv, dh, dh if rot is None else rot,
-            base, eps, io, _ptr(workspace, "workspace"),
+            *views, _p(w_q, "w_q", dt, (dh,), dev, True), _p(w_k, "w_k", dt, (dh,), dev, True),
+            _p(positions, "positions", torch.int32, (B, T), dev, True),
+            _p(dq_out, "dq_out", dt, (B, T, Hq, dh), dev),
+            _p(dk_out, "dk_out", dt, (B, T, Hkv, dh), dev),
+            _p(g["dq"], "dq", dt, (B, T, Hq, dh), dev), _p(g["dk"], "dk", dt, (B, T, Hkv, dh), dev),
+            _p(g["dw_q"], "dw_q", f32, (dh,), dev), _p(g["dw_k"], "dw_k", f32, (dh,), dev),
+            B, T, Hq, Hkv, dh, dh if rot is None else rot, base, eps, io,
+            _p(workspace, "workspace", None, None, dev),
             workspace.numel() * workspace.element_size(), st), "rglru_qk_norm_rope_bwd")
     return g
 
@@ -212,28 +253,21 @@ def rglru_local_attn_fwd(q, k, v, *, window=0, sinks=0, scale=None, lens=None, o
     1 / sqrt(dh) by default. With `lens` (B, int32; S == T) row b has lens[b] tokens, and rows
     past them are left as they were in given outputs, zeros (and -inf in lse) in ones allocated
     here. Returns (out, lse), lse (B, Hq, T) or None when it is neither wanted nor given."""
-    B, T, Hq, dh = _heads(q, "q")
-    _, S, Hkv, _ = _heads(k, "k", q)
-    _heads(v, "v", q)
-    _shape(k, "k", (B, S, Hkv, dh))
-    _shape(v, "v", (B, S, Hkv, dh))
-    dt, dev = q.dtype, q.device
-    io = _io_of(dt)
-    _same_device(dev, k=k, v=v, lens=lens, out=out, lse=lse, dev_status=dev_status)
+    views, dev, dt, io, B, T, S, Hq, Hkv, dh = _sizes(q, k, v)
     with _on(dev, stream) as st:
         if out is None:
             make = torch.empty if lens is None else torch.zeros
-            out = make((B, T, Hq, dh), device=dev, dtype=dt)
+            out = make((B, T, Hq, dh), device=q.device, dtype=dt)
         if lse is None and want_lse:
-            lse = torch.empty((B, Hq, T), device=dev, dtype=torch.float32)
+            lse = torch.empty((B, Hq, T), device=q.device, dtype=torch.float32)
             if lens is not None:
                 lse.fill_(float("-inf"))
         _check(LIB.rglru_local_attn_fwd(
-            *_view(q), *_view(k), *_view(v), _ptr(lens, "lens", torch.int32, (B,), optional=True),
-            _ptr(out, "out", dt, (B, T, Hq, dh)),
-            _ptr(lse, "lse", torch.float32, (B, Hq, T), optional=True), B, T, S, Hq, Hkv, dh,
+            *views, _p(lens, "lens", torch.int32, (B,), dev, True),
+            _p(out, "out", dt, (B, T, Hq, dh), dev),
+            _p(lse, "lse", torch.float32, (B, Hq, T), dev, True), B, T, S, Hq, Hkv, dh,
             window, sinks, dh ** -0.5 if scale is None else scale, io,
-            _ptr(dev_status, "dev_status", torch.int32, optional=True), st),
+            _p(dev_status, "dev_status", torch.int32, None, dev, True), st),
             "rglru_local_attn_fwd")
     return out, lse
 
@@ -243,33 +277,26 @@ def rglru_local_attn_bwd(q, k, v, out, lse, dout, *, window=0, sinks=0, scale=No
     """Backward of rglru_local_attn_fwd from its inputs, its out and lse, and dout. Returns a
     dict with dq, dk, dv (dense, the I/O dtype). `grads` may hold preallocated outputs by name;
     with `lens`, rows past a sequence are left as they were there, zeros otherwise."""
-    B, T, Hq, dh = _heads(q, "q")
-    _, S, Hkv, _ = _heads(k, "k", q)
-    _heads(v, "v", q)
-    _shape(k, "k", (B, S, Hkv, dh))
-    _shape(v, "v", (B, S, Hkv, dh))
-    dt, dev = q.dtype, q.device
-    io = _io_of(dt)
+    views, dev, dt, io, B, T, S, Hq, Hkv, dh = _sizes(q, k, v)
     g = dict(grads or {})
-    _same_device(dev, k=k, v=v, out=out, lse=lse, dout=dout, lens=lens, workspace=workspace,
-                 dev_status=dev_status, **g)
     with _on(dev, stream) as st:
         make = torch.empty if lens is None else torch.zeros
         for name, shape in (("dq", (B, T, Hq, dh)), ("dk", (B, S, Hkv, dh)),
                             ("dv", (B, S, Hkv, dh))):
             if g.get(name) is None:
-                g[name] = make(shape, device=dev, dtype=dt)
+                g[name] = make(shape, device=q.device, dtype=dt)
         need = LIB.rglru_local_attn_bwd_workspace_bytes(B, T, S, Hq, Hkv, dh, window, sinks, io)
-        workspace = _workspace(workspace, need, dev)
+        workspace = _workspace(workspace, need, q.device)
         _check(LIB.rglru_local_attn_bwd(
-            *_view(q), *_view(k), *_view(v), _ptr(out, "out", dt, (B, T, Hq, dh)),
-            _ptr(lse, "lse", torch.float32, (B, Hq, T)), _ptr(dout, "dout", dt, (B, T, Hq, dh)),
-            _ptr(lens, "lens", torch.int32, (B,), optional=True),
-            _ptr(g["dq"], "dq", dt, (B, T, Hq, dh)), _ptr(g["dk"], "dk", dt, (B, S, Hkv, dh)),
-            _ptr(g["dv"], "dv", dt, (B, S, Hkv, dh)), B, T, S, Hq, Hkv, dh, window, sinks,
-            dh ** -0.5 if scale is None else scale, io, _ptr(workspace, "workspace"),
+            *views, _p(out, "out", dt, (B, T, Hq, dh), dev),
+            _p(lse, "lse", torch.float32, (B, Hq, T), dev),
+            _p(dout, "dout", dt, (B, T, Hq, dh), dev),
+            _p(lens, "lens", torch.int32, (B,), dev, True),
+            _p(g["dq"], "dq", dt, (B, T, Hq, dh), dev), _p(g["dk"], "dk", dt, (B, S, Hkv, dh), dev),
+            _p(g["dv"], "dv", dt, (B, S, Hkv, dh), dev), B, T, S, Hq, Hkv, dh, window, sinks,
+            dh ** -0.5 if scale is None else scale, io, _p(workspace, "workspace", None, None, dev),
             workspace.numel() * workspace.element_size(),
-            _ptr(dev_status, "dev_status", torch.int32, optional=True), st),
+            _p(dev_status, "dev_status", torch.int32, None, dev, True), st),
             "rglru_local_attn_bwd")
     return g
 
@@ -279,32 +306,28 @@ def rglru_paged_attn_decode(q, k_cache, v_cache, page_table, lens, *, window=0, 
     """Attention of one new token of each sequence, q (B, Hq, dh), over its paged cache (pages,
     page_size, Hkv, dh): its last `window` keys (0: all) and its first `sinks`, of lens[b] keys
     (the new token's own among them; 0: the row of out is zeros). Returns out (B, Hq, dh)."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor (the library has no CPU path)")
+    qp = _p(q, "q", None, None, None)
     if q.dim() != 3:
         raise ValueError("q must be (B, Hq, dh)")
     B, Hq, dh = q.shape
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, q.get_device()
     io = _io_of(dt)
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, page_table=page_table, lens=lens, out=out,
-                 workspace=workspace, dev_status=dev_status)
-    if k_cache.dim() != 4:
-        raise ValueError("a cache must be (pages, page_size, Hkv, dh)")
-    Hkv = k_cache.shape[2]
-    pages, page_size, max_pages = _cache_sizes(k_cache, v_cache, page_table, B, Hkv, dh)
+    _place(k_cache, "k_cache", dev)
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    kc, vc, table, pages, page_size, max_pages = _cache(k_cache, v_cache, page_table, dt, B, Hkv,
+                                                        dh, dev)
     with _on(dev, stream) as st:
         if out is None:
-            out = torch.empty((B, Hq, dh), device=dev, dtype=dt)
+            out = torch.empty((B, Hq, dh), device=q.device, dtype=dt)
         need = LIB.rglru_paged_attn_decode_workspace_bytes(B, Hq, Hkv, dh, page_size, max_pages,
                                                            window, sinks, io)
-        workspace = _workspace(workspace, need, dev)
+        workspace = _workspace(workspace, need, q.device)
         _check(LIB.rglru_paged_attn_decode(
-            _ptr(q, "q", dt, (B, Hq, dh)), _ptr(k_cache, "k_cache", dt),
-            _ptr(v_cache, "v_cache", dt), _ptr(page_table, "page_table", torch.int32),
-            _ptr(lens, "lens", torch.int32, (B,)), _ptr(out, "out", dt, (B, Hq, dh)), pages,
-            page_size, max_pages, B, Hq, Hkv, dh, window, sinks,
-            dh ** -0.5 if scale is None else scale, io, _ptr(workspace, "workspace"),
+            qp, kc, vc, table, _p(lens, "lens", torch.int32, (B,), dev),
+            _p(out, "out", dt, (B, Hq, dh), dev), pages, page_size, max_pages, B, Hq, Hkv, dh,
+            window, sinks, dh ** -0.5 if scale is None else scale, io,
+            _p(workspace, "workspace", None, None, dev),
             workspace.numel() * workspace.element_size(),
-            _ptr(dev_status, "dev_status", torch.int32, optional=True), st),
+            _p(dev_status, "dev_status", torch.int32, None, dev, True), st),
             "rglru_paged_attn_decode")
     return out

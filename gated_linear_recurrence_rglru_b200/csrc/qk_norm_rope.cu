@@ -11,8 +11,9 @@
 // Bound by HBM: x (and dy) read once, y (dx) written once. One warp takes one
 // token and a run of its heads; a lane holds 8 consecutive elements of a row
 // (16 bytes of bf16), a row is dh/8 lanes, so narrow heads put several rows in
-// a warp. Norm sums are warp shuffles; the rotation's partner sits rot/16 lanes
-// away at the same place of its lane (rot is a multiple of 16), one shuffle.
+// a warp, and a lane has 64 bytes of loads in flight. Norm sums are warp shuffles;
+// the rotation's partner sits rot/16 lanes away at the same place of its lane (rot
+// is a multiple of 16), one shuffle.
 // Sine and cosine are formed once per token and warp for all of the run's
 // heads. The angle of pair i is position * phase[i] in 64-bit integers, phase
 // a fraction of a turn times 2^64: the product modulo 2^64 is the exact
@@ -27,22 +28,36 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxBlocks = 148 * 6;
-constexpr int kBwdBlocks = 148 * 4;   // each leaves one partial sum of dw
+// Rows that a lane has in flight: 64 bytes (of q; as much of dy in the backward).
+template <typename T> constexpr int rows_in_flight() { return 8 / sizeof(T); }
+constexpr int kMaxBlocks = 148 * 3;   // resident at once
+constexpr int kBwdBlocks = 148 * 2;   // resident at once; each leaves one partial sum of dw
+
+// 8 elements of a row: as loaded, and as floats.
+template <typename T> struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
 
 struct Row8 {
   float v[8];
 };
 
-__device__ __forceinline__ Row8 load8(const float *p) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+template <typename T> __device__ __forceinline__ Raw<T> load_raw(const T *p, bool live) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    r.w[i] = live ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+  return r;
 }
 
-__device__ __forceinline__ Row8 load8(const __nv_bfloat16 *p) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ Row8 floats(const Raw<float> &a) {
+  return {{__uint_as_float(a.w[0].x), __uint_as_float(a.w[0].y), __uint_as_float(a.w[0].z),
+           __uint_as_float(a.w[0].w), __uint_as_float(a.w[1].x), __uint_as_float(a.w[1].y),
+           __uint_as_float(a.w[1].z), __uint_as_float(a.w[1].w)}};
+}
+
+__device__ __forceinline__ Row8 floats(const Raw<__nv_bfloat16> &a) {
+  const uint32_t w[4] = {a.w[0].x, a.w[0].y, a.w[0].z, a.w[0].w};
   Row8 r;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -67,13 +82,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const Row8 &r) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 8 elements moved as they are (v into its cache).
-__device__ __forceinline__ void copy8(float *d, const float *s) {
-  reinterpret_cast<float4 *>(d)[0] = __ldg(reinterpret_cast<const float4 *>(s));
-  reinterpret_cast<float4 *>(d)[1] = __ldg(reinterpret_cast<const float4 *>(s) + 1);
-}
-__device__ __forceinline__ void copy8(__nv_bfloat16 *d, const __nv_bfloat16 *s) {
-  *reinterpret_cast<uint4 *>(d) = __ldg(reinterpret_cast<const uint4 *>(s));
+// Moved as they are (v into its cache).
+template <typename T> __device__ __forceinline__ void store_raw(T *d, const Raw<T> &r) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4 *>(d)[i] = r.w[i];
 }
 
 template <int LPR> __device__ __forceinline__ float row_sum(float v) {
@@ -134,145 +146,196 @@ __device__ __forceinline__ void stage_phases(unsigned long long *dst, const QkAr
   for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) dst[i] = p.phase[i];
 }
 
+// This lane's weights, kept as loaded (half the registers in bf16).
 template <typename T>
-__device__ __forceinline__ Row8 weights(const void *w, int e0, bool in) {
-  Row8 r;
+__device__ __forceinline__ Raw<T> weights(const void *w, int e0, bool in) {
+  if (w != nullptr) return load_raw(static_cast<const T *>(w) + e0, in);
+  const uint32_t one = sizeof(T) == 4 ? 0x3F800000u : 0x3F803F80u;
+  Raw<T> r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r.v[e] = 1.0f;
-  if (w != nullptr && in) r = load8(static_cast<const T *>(w) + e0);
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) r.w[i] = make_uint4(one, one, one, one);
   return r;
 }
 
-// Forward (kAppend: k and v rows go to the cache). Work item: one token and one
-// of n_runs runs of `run` heads of the list q heads, k heads.
+// Rows h0 .. h1-1 (heads of one token) normed and rotated: src and dst at the
+// token's head 0 and this lane's elements, sh and dh elements between heads.
+template <typename T, int LPR>
+__device__ __forceinline__ void norm_rows(const T *src, long long sh, T *dst, int dh, int h0, int h1,
+                                          const Place<LPR> &at, const Raw<T> &raw_w,
+                                          const Turn &turn, float inv, float eps) {
+  constexpr int R = 32 / LPR, kRows = rows_in_flight<T>();
+  const Row8 w = floats(raw_w);
+  for (int h = h0; h < h1; h += R * kRows) {
+    Raw<T> raw[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int hh = h + u * R + at.sub;
+      raw[u] = load_raw(src + hh * sh, at.in && hh < h1);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int hh = h + u * R + at.sub;
+      if (h + u * R >= h1) break;                       // (the warp's rows all past the end)
+      Row8 x = floats(raw[u]);
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
+      const float r = rsqrtf(row_sum<LPR>(ss) * inv + eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.v[e] *= r * w.v[e];
+      rotate(x, turn);
+      if (at.in && hh < h1) store8(dst + static_cast<long long>(hh) * dh, x);
+    }
+  }
+}
+
+// Their backward: dw is added to, dx written; dy and dx dense.
+template <typename T, int LPR>
+__device__ __forceinline__ void grad_rows(const T *src, long long sh, const T *dy, T *dx, int dh, int h0,
+                                          int h1, const Place<LPR> &at, const Raw<T> &raw_w, Row8 &dw,
+                                          const Turn &turn, float inv, float eps) {
+  constexpr int R = 32 / LPR, kRows = rows_in_flight<T>();
+  const Row8 w = floats(raw_w);
+  for (int h = h0; h < h1; h += R * kRows) {
+    Raw<T> raw[kRows], rawg[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int hh = h + u * R + at.sub;
+      const bool live = at.in && hh < h1;
+      raw[u] = load_raw(src + hh * sh, live);
+      rawg[u] = load_raw(dy + static_cast<long long>(hh) * dh, live);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int hh = h + u * R + at.sub;
+      if (h + u * R >= h1) break;
+      const Row8 x = floats(raw[u]);
+      Row8 g = floats(rawg[u]);
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
+      const float r = rsqrtf(row_sum<LPR>(ss) * inv + eps);
+      rotate(g, turn);
+      float gx = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw.v[e] = fmaf(g.v[e], x.v[e] * r, dw.v[e]);
+        g.v[e] *= w.v[e];
+        gx = fmaf(g.v[e], x.v[e], gx);
+      }
+      const float c = row_sum<LPR>(gx) * inv * r * r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g.v[e] = r * (g.v[e] - x.v[e] * c);
+      if (at.in && hh < h1) store8(dx + static_cast<long long>(hh) * dh, g);
+    }
+  }
+}
+
+// Work item: one token and one of n_runs runs of `run` heads of the list q heads,
+// k heads. Tokens times runs stay below 2^31 (there is more than one run only
+// where tokens are few).
+struct Item {
+  unsigned tok;
+  int b, t, h0, h1;
+  __device__ Item(const QkArgs &p, unsigned it, int run, int n_runs) {
+    tok = it;
+    h0 = 0;
+    if (n_runs > 1) {
+      tok = it / static_cast<unsigned>(n_runs);
+      h0 = static_cast<int>(it - tok * static_cast<unsigned>(n_runs)) * run;
+    }
+    b = static_cast<int>(tok / static_cast<unsigned>(p.T));
+    t = static_cast<int>(tok - static_cast<unsigned>(b) * static_cast<unsigned>(p.T));
+    h1 = min(h0 + run, p.Hq + p.Hkv);
+  }
+};
+
+template <typename T> __device__ __forceinline__ const T *token_of(const Strided &x, const Item &i, int e0) {
+  return static_cast<const T *>(x.p) + i.b * x.sb + i.t * x.st + e0;
+}
+
+// Forward (kAppend: k and v rows go to the cache).
 template <typename T, int LPR, bool kAppend>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkArgs p,
-                                                          int run, int n_runs) {
+__global__ void __launch_bounds__(kThreads, 3) qk_fwd_kernel(const __grid_constant__ QkArgs p,
+                                                             int run, int n_runs) {
   __shared__ unsigned long long phase[kMaxPairs];
   stage_phases(phase, p);
   __syncthreads();
   constexpr int R = 32 / LPR;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Place<LPR> at(lane, p.dh);
-  const Row8 wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
+  const Raw<T> wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
   Turn turn = make_turn<LPR>(lane, at.e0, p.rot);
-  const int heads = p.Hq + p.Hkv;
   const float inv = 1.0f / static_cast<float>(p.dh);
-  const long long items = static_cast<long long>(p.B) * p.T * n_runs;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items;
-       it += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long tok = it / n_runs;
-    const int h0 = static_cast<int>(it % n_runs) * run;
-    const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
-    const int pos = p.positions ? __ldg(p.positions + tok) : t;
+  const unsigned items = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.T) * n_runs;
+  for (unsigned x = blockIdx.x * kWarps + warp; x < items; x += gridDim.x * kWarps) {
+    const Item it(p, x, run, n_runs);
+    const int pos = p.positions ? __ldg(p.positions + it.tok) : it.t;
+    T *q_out = static_cast<T *>(p.q_out) + static_cast<long long>(it.tok) * p.Hq * p.dh + at.e0;
+    T *k_out = nullptr;
     long long slot = 0;
-    bool stored = true;                                 // whether the token has a cache slot
+    const int k0 = max(it.h0 - p.Hq, 0), k1 = it.h1 - p.Hq;
     if (kAppend) {
-      if (pos < 0) continue;                            // padding (the warp's one token)
+      if (pos < 0) {                                    // padding (the warp's one token)
+        for (int h = it.h0 + at.sub; h < min(it.h1, p.Hq); h += R)
+          if (at.in) store8(q_out + static_cast<long long>(h) * p.dh, Row8{});
+        continue;
+      }
       const int pg = pos / p.page_size;
       const int page = pg < p.max_pages
-                           ? __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + pg)
+                           ? __ldg(p.page_table + static_cast<long long>(it.b) * p.max_pages + pg)
                            : -1;
-      stored = page >= 0 && page < p.num_pages;
-      if (!stored && p.dev_status && lane == 0)
+      if (page >= 0 && page < p.num_pages) {
+        slot = (static_cast<long long>(page) * p.page_size + pos % p.page_size) * p.Hkv * p.dh + at.e0;
+        k_out = static_cast<T *>(p.k_cache) + slot;
+      } else if (p.dev_status && lane == 0) {
         atomicCAS(p.dev_status, 0, RGLRU_ERR_INVALID_ARG);
-      slot = (static_cast<long long>(page) * p.page_size + pos % p.page_size) * p.Hkv;
+      }
+    } else {
+      k_out = static_cast<T *>(p.k_out) + static_cast<long long>(it.tok) * p.Hkv * p.dh + at.e0;
     }
     set_turn(turn, phase, pos, at.e0, p.rot / 2, false);
-    const int h1 = min(h0 + run, heads);
-#pragma unroll 2
-    for (int h = h0; h < h1; h += R) {
-      const int hh = h + at.sub;
-      const bool live = at.in && hh < h1;
-      const bool is_q = hh < p.Hq;
-      const int hk = hh - p.Hq;
-      Row8 x = {};
-      if (live) {
-        const T *src = is_q ? static_cast<const T *>(p.q.p) + b * p.q.sb + t * p.q.st + hh * p.q.sh
-                            : static_cast<const T *>(p.k.p) + b * p.k.sb + t * p.k.st + hk * p.k.sh;
-        x = load8(src + at.e0);
-      }
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * inv + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x.v[e] *= r * (is_q ? wq.v[e] : wk.v[e]);
-      rotate(x, turn);
-      if (!live) continue;
-      if (is_q) {
-        store8(static_cast<T *>(p.q_out) + (tok * p.Hq + hh) * p.dh + at.e0, x);
-      } else if (!kAppend) {
-        store8(static_cast<T *>(p.k_out) + (tok * p.Hkv + hk) * p.dh + at.e0, x);
-      } else if (stored) {
-        store8(static_cast<T *>(p.k_cache) + (slot + hk) * p.dh + at.e0, x);
-        copy8(static_cast<T *>(p.v_cache) + (slot + hk) * p.dh + at.e0,
-              static_cast<const T *>(p.v.p) + b * p.v.sb + t * p.v.st + hk * p.v.sh + at.e0);
-      }
+    norm_rows<T, LPR>(token_of<T>(p.q, it, at.e0), p.q.sh, q_out, p.dh, it.h0, min(it.h1, p.Hq), at, wq,
+                      turn, inv, p.eps);
+    if (k_out == nullptr) continue;                     // no cache slot (the warp's one token)
+    norm_rows<T, LPR>(token_of<T>(p.k, it, at.e0), p.k.sh, k_out, p.dh, k0, k1, at, wk, turn, inv, p.eps);
+    if (kAppend) {
+      const T *v = token_of<T>(p.v, it, at.e0);
+      for (int h = k0 + at.sub; h < k1; h += R)
+        if (at.in)
+          store_raw(static_cast<T *>(p.v_cache) + slot + static_cast<long long>(h) * p.dh,
+                    load_raw(v + h * p.v.sh, true));
     }
   }
 }
 
 // Backward; each block leaves its sums of dw_q and dw_k in partial[block][2][dh].
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const __grid_constant__ QkArgs p,
-                                                          int run, int n_runs, float *partial) {
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const __grid_constant__ QkArgs p,
+                                                             int run, int n_runs, float *partial) {
   __shared__ unsigned long long phase[kMaxPairs];
   __shared__ float sums[kWarps][2][256 + 8];
   stage_phases(phase, p);
   __syncthreads();
-  constexpr int R = 32 / LPR;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Place<LPR> at(lane, p.dh);
-  const Row8 wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
+  const Raw<T> wq = weights<T>(p.w_q, at.e0, at.in), wk = weights<T>(p.w_k, at.e0, at.in);
   Turn turn = make_turn<LPR>(lane, at.e0, p.rot);
   Row8 dwq = {}, dwk = {};
-  const int heads = p.Hq + p.Hkv;
   const float inv = 1.0f / static_cast<float>(p.dh);
-  const long long items = static_cast<long long>(p.B) * p.T * n_runs;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items;
-       it += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long tok = it / n_runs;
-    const int h0 = static_cast<int>(it % n_runs) * run;
-    const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
-    const int pos = p.positions ? __ldg(p.positions + tok) : t;
+  const unsigned items = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.T) * n_runs;
+  for (unsigned x = blockIdx.x * kWarps + warp; x < items; x += gridDim.x * kWarps) {
+    const Item it(p, x, run, n_runs);
+    const int pos = p.positions ? __ldg(p.positions + it.tok) : it.t;
     set_turn(turn, phase, pos, at.e0, p.rot / 2, true);
-    const int h1 = min(h0 + run, heads);
-#pragma unroll 2
-    for (int h = h0; h < h1; h += R) {
-      const int hh = h + at.sub;
-      const bool live = at.in && hh < h1;
-      const bool is_q = hh < p.Hq;
-      const int hk = hh - p.Hq;
-      const long long row = is_q ? tok * p.Hq + hh : tok * p.Hkv + hk;
-      Row8 x = {}, g = {};
-      if (live) {
-        const T *src = is_q ? static_cast<const T *>(p.q.p) + b * p.q.sb + t * p.q.st + hh * p.q.sh
-                            : static_cast<const T *>(p.k.p) + b * p.k.sb + t * p.k.st + hk * p.k.sh;
-        x = load8(src + at.e0);
-        g = load8(static_cast<const T *>(is_q ? p.dq_out : p.dk_out) + row * p.dh + at.e0);
-      }
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * inv + p.eps);
-      rotate(g, turn);
-      float gx = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = g.v[e] * (x.v[e] * r);
-        if (is_q)
-          dwq.v[e] += d;
-        else
-          dwk.v[e] += d;
-        g.v[e] *= is_q ? wq.v[e] : wk.v[e];
-        gx = fmaf(g.v[e], x.v[e], gx);
-      }
-      const float c = row_sum<LPR>(gx) * inv * r * r;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g.v[e] = r * (g.v[e] - x.v[e] * c);
-      if (live) store8(static_cast<T *>(is_q ? p.q_out : p.k_out) + row * p.dh + at.e0, g);
-    }
+    const long long oq = static_cast<long long>(it.tok) * p.Hq * p.dh + at.e0;
+    const long long ok = static_cast<long long>(it.tok) * p.Hkv * p.dh + at.e0;
+    grad_rows<T, LPR>(token_of<T>(p.q, it, at.e0), p.q.sh, static_cast<const T *>(p.dq_out) + oq,
+                      static_cast<T *>(p.q_out) + oq, p.dh, it.h0, min(it.h1, p.Hq), at, wq, dwq, turn,
+                      inv, p.eps);
+    grad_rows<T, LPR>(token_of<T>(p.k, it, at.e0), p.k.sh, static_cast<const T *>(p.dk_out) + ok,
+                      static_cast<T *>(p.k_out) + ok, p.dh, max(it.h0 - p.Hq, 0), it.h1 - p.Hq, at, wk,
+                      dwk, turn, inv, p.eps);
   }
   // rows of one warp (lanes LPR apart hold the same elements), then the warps
 #pragma unroll

@@ -70,7 +70,8 @@ int rglru_qk_norm_rope_fwd(const void *q, const rglru_strides *q_strides, const 
  * page_table[b * max_pages + p / page_size], slot p % page_size.
  *   k_cache, v_cache (num_pages, page_size, Hkv, dh)  io, written in place
  *   page_table (B, max_pages) int; positions (B, T) int, required
- * A token at a negative position is padding: nothing of it is read or written.
+ * A token at a negative position is padding: it is not read, its row of q_out
+ * becomes zeros and no slot is written.
  * Two tokens of a call with the same slot leave either one's values there.
  */
 int rglru_qk_norm_rope_append(const void *q, const rglru_strides *q_strides, const void *k,
