@@ -103,6 +103,15 @@ struct Turn {
   int partner;
 };
 
+// Sine and cosine of pi x, |x| <= 1: to the last places for fp32 rows; for bf16
+// rows by the hardware's instructions, off by at most 2^-21 on this range, far
+// below the 2^-8 of the row's own rounding (48 -> 45 us on 185 MB).
+__device__ __forceinline__ void turn_of(float x, float &s, float &c, float) { sincospif(x, &s, &c); }
+__device__ __forceinline__ void turn_of(float x, float &s, float &c, __nv_bfloat16) {
+  __sincosf(x * 3.14159265358979f, &s, &c);
+}
+
+template <typename T>
 __device__ __forceinline__ void set_turn(Turn &t, const unsigned long long *phase, int pos, int e0,
                                          int half, bool back) {
   if (!t.on) return;
@@ -114,7 +123,7 @@ __device__ __forceinline__ void set_turn(Turn &t, const unsigned long long *phas
         phase[i0 + e] * static_cast<unsigned long long>(static_cast<long long>(pos));
     // the top 32 bits as a signed fraction of a turn, -1/2 .. 1/2
     const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
-    sincospif(x, &t.s[e], &t.c[e]);   // angle = pi x, x = 2 * fraction
+    turn_of(x, t.s[e], t.c[e], T());  // angle = pi x, x = 2 * fraction
     if (first != back) t.s[e] = -t.s[e];
   }
 }
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_fwd_kernel(const __grid_consta
     } else {
       k_out = static_cast<T *>(p.k_out) + static_cast<long long>(it.tok) * p.Hkv * p.dh + at.e0;
     }
-    set_turn(turn, phase, pos, at.e0, p.rot / 2, false);
+    set_turn<T>(turn, phase, pos, at.e0, p.rot / 2, false);
     norm_rows<T, LPR>(token_of<T>(p.q, it, at.e0), p.q.sh, q_out, p.dh, it.h0, min(it.h1, p.Hq), at, wq,
                       turn, inv, p.eps);
     if (k_out == nullptr) continue;                     // no cache slot (the warp's one token)
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const __grid_consta
   for (unsigned x = blockIdx.x * kWarps + warp; x < items; x += gridDim.x * kWarps) {
     const Item it(p, x, run, n_runs);
     const int pos = p.positions ? __ldg(p.positions + it.tok) : it.t;
-    set_turn(turn, phase, pos, at.e0, p.rot / 2, true);
+    set_turn<T>(turn, phase, pos, at.e0, p.rot / 2, true);
     const long long oq = static_cast<long long>(it.tok) * p.Hq * p.dh + at.e0;
     const long long ok = static_cast<long long>(it.tok) * p.Hkv * p.dh + at.e0;
     grad_rows<T, LPR>(token_of<T>(p.q, it, at.e0), p.q.sh, static_cast<const T *>(p.dq_out) + oq,
