@@ -13,6 +13,8 @@
 // decode_join_kernel joins them in the order of the chunks.
 //
 // A key whose page number is out of range is hidden (and reported).
+#include <math.h>
+
 #include "attn_kernels.h"
 #include "common.cuh"
 
@@ -595,10 +597,15 @@ int slices_of(const DecodeArgs &p, int io) {
   return ceil_div(p.Hq / p.Hkv, tensor_path(p, io) ? 16 : kGenHeads);
 }
 
-// Keys of a chunk: enough chunks for about two waves of resident blocks when
-// every sequence has as many keys as its table and window allow, in whole
-// 64-key steps, at least 256 keys (shorter chunks spend more on their start
-// and their part than on their keys).
+// Keys of a chunk. More chunks fill the GPU and even out ragged sequences; each
+// costs its block a start and an end (the chain length, page table, first keys,
+// and the joining of its warps: about 3 us) and more than one costs the join (5
+// us). The time of every number of chunks is estimated for sequences as long as
+// their tables and window allow, in waves of resident blocks that share HBM (44
+// bytes a ns and SM; 60 for an SM that runs beside idle ones), and the most chunks
+// within 5 % of the best are taken: 128 sequences of 1028 visible 256-wide keys
+// get one chunk (three took 47 us, one 30), 4 sequences of 131072 keys, ragged,
+// get 74 rather than 37 (146 and 133 us).
 Parts parts_of(const DecodeArgs &p, int io) {
   const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
   long long most = cap;
@@ -606,15 +613,25 @@ Parts parts_of(const DecodeArgs &p, int io) {
     most = static_cast<long long>(p.window) + p.sinks;
   const long long units = static_cast<long long>(p.B) * p.Hkv * slices_of(p, io);
   const int resident = !tensor_path(p, io) ? 1 : p.dh == 256 ? 1 : p.dh == 128 ? 2 : 4;
-  const long long want = (2ll * 148 * resident + units - 1) / units;   // chunks a unit
-  long long chunk = (most + want - 1) / want;
-  chunk = (chunk + 63) / 64 * 64;
-  if (chunk < 256) chunk = 256;
+  const double slots = 148.0 * resident, key_bytes = 2.0 * p.dh * (io == RGLRU_IO_F32 ? 4 : 2);
+  auto chunk_of = [&](long long chunks) { return ((most + chunks - 1) / chunks + 63) / 64 * 64; };
+  auto time_of = [&](long long chunks) {               // ns
+    const double blocks = static_cast<double>(units) * chunks;
+    const double waves = ceil(blocks / slots);
+    const double share = blocks < slots ? fmin(60.0, 44.0 * slots / blocks) : 44.0;
+    return waves * (3000.0 + chunk_of(chunks) * key_bytes / (share / resident)) + (chunks > 1 ? 5000.0 : 0.0);
+  };
+  const long long limit = most / 128 > 1 ? (most / 128 < 1024 ? most / 128 : 1024) : 1;
+  double best = time_of(1);
+  for (long long c = 2; c <= limit; c += 1 + c / 16) best = fmin(best, time_of(c));
+  long long chunks = 1;
+  for (long long c = 1; c <= limit; c += 1 + c / 16)
+    if (time_of(c) <= 1.05 * best) chunks = c;
   Parts r;
   r.o = nullptr;
   r.ml = nullptr;
-  r.chunk = static_cast<int>(chunk);
-  r.chunks = static_cast<int>((most + chunk - 1) / chunk);
+  r.chunk = static_cast<int>(chunk_of(chunks));
+  r.chunks = static_cast<int>((most + r.chunk - 1) / r.chunk);
   return r;
 }
 
