@@ -73,8 +73,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       : "memory");
 }
 
-// The 256 threads of warps 0-7 meet.
-__device__ __forceinline__ void bar_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A warp group's registers a thread from here on: more (N > 0) or fewer (N < 0).
+template <int N> __device__ __forceinline__ void set_registers() {
+  if constexpr (N > 0)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(-N));
+}
+
+// The 256 threads of one of two groups of eight warps meet.
+__device__ __forceinline__ void bar_sync_group(int group) {
+  asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory");
+}
 
 // 16 consecutive TMEM columns of this thread's lane, as raw words.
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -138,6 +148,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 2^a, 2^b for a, b <= 127 on the FMA pipes: 2^x = 2^n 2^f with n the nearest whole
+// number (read off the low bits of x + 1.5 * 2^23) and f in [-1/2, 1/2], 2^f by the
+// polynomial of degree 4 of least relative error there (2.6e-6, by Remez exchange),
+// n added to the exponent. Below -126 the result is 2^-126 to a factor of sqrt 2.
+__device__ __forceinline__ void ex2_pair(float &a, float &b) {
+  constexpr float kMagic = 12582912.0f;
+  const unsigned long long x = pair(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+  const unsigned long long z = add2(x, pair(kMagic, kMagic));
+  const unsigned long long n = add2(z, pair(-kMagic, -kMagic));
+  const unsigned long long f = fma2(n, pair(-1.0f, -1.0f), x);
+  unsigned long long r = fma2(f, pair(9.570101911e-03f, 9.570101911e-03f), pair(5.591786032e-02f, 5.591786032e-02f));
+  r = fma2(r, f, pair(2.402474483e-01f, 2.402474483e-01f));
+  r = fma2(r, f, pair(6.931218147e-01f, 6.931218147e-01f));
+  r = fma2(r, f, pair(9.999992614e-01f, 9.999992614e-01f));
+  float za, zb, ra, rb;
+  unpair(z, za, zb);
+  unpair(r, ra, rb);
+  a = __int_as_float(__float_as_int(ra) + (__float_as_int(za) << 23));
+  b = __int_as_float(__float_as_int(rb) + (__float_as_int(zb) << 23));
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -160,6 +191,13 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16 *dst, const float (&v)
     for (int q = 0; q < 4; ++q)
       reinterpret_cast<uint4 *>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   }
+}
+
+// Bits lo .. hi (ends included, any values) of 32.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const uint32_t upto = hi >= 31 ? 0xFFFFFFFFu : hi < 0 ? 0u : (2u << hi) - 1u;
+  const uint32_t from = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+  return upto & from;
 }
 
 // Keys that no query of the call sees: [sinks, dead_lo) and [nk, S). Their rows

@@ -315,7 +315,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       step_at<kKeys, kBN>(wk, G, i, h, t0);
       float next = 0.0f;
       if (kKeys) {
-        bar_sync_softmax();                                // this step's stats are there
+        bar_sync_group(0);                                // this step's stats are there
         if (i + 1 < wk.n) next = load_stat(i + 1);
       }
       const int sb = i % C::kNS;

@@ -4,23 +4,26 @@
 //   S = Q K^T (128 queries x 128 keys), p = 2^(S c - m), c = scale log2 e,
 //   l = l 2^(m - m') + sum p,  O = O 2^(m - m') + P V,  out = O / l
 //
-// One block takes 128 queries of one head and walks the key tiles that its mask
-// leaves. Warps 0-7 are the softmax, thread = query row = TMEM lane, warp group
-// g the columns 64 g ..: a row's maximum is one exchange through shared memory
-// between two threads. Warp 8 issues the TMA copies (K and V through one ring of
-// slots, 128 keys x up to 128 columns each, in the order of use), warp 9 the
-// MMAs: S from shared memory (Q and K both K-major), P V with P as the TMEM
-// operand (bf16, written over the scores it came from) and V MN-major as TMA
-// left it. The accumulator O
-// stays in TMEM for the whole walk; the reference maximum m moves only when it
-// is 8 or more behind in log2 units (weights up to 2^8 keep their relative
-// precision), so O is seldom rescaled.
+// Blocks are resident, one an SM, and take unit after unit: 128-query tiles of a
+// head and the key tiles that their mask leaves, the next unit's copies and first
+// scores running while the softmax warps store the last one's rows. Heads 64 and
+// 128 wide: a block works on two query tiles at once, which share every K and V
+// tile (two heads of a group, or two tiles of one head), and take turns: while the
+// softmax works on one's scores, the tensor core does the other's P V and next S.
+// 256 wide: one query tile (O takes 256 TMEM columns) with two score buffers, S of
+// the next key tile is made while the softmax works on this one.
 //
-// Heads 64 and 128 wide: one score buffer, 256 TMEM columns and under half the
-// shared memory a block, so two blocks share an SM and one's softmax runs under
-// the other's MMAs. 256 wide: O takes 256 columns; one block an SM with two
-// score buffers, S of the next tile is made while the softmax works on this one.
-// Only tiles that the mask cuts test it, element by element.
+// Eight softmax warps, thread = query row = TMEM lane: with two query tiles a thread
+// has all 128 scores of its row and key tile in registers; with one, two warp groups
+// share the columns, and a row's maximum is one exchange through shared memory
+// between two threads. One warp issues the TMA copies (K and V through one
+// ring of slots, 128 keys x up to 128 columns each, in the order of use), one the
+// MMAs: S from shared memory (Q and K both K-major), P V with P as the TMEM operand
+// (bf16, written over the scores it came from) and V MN-major as TMA left it. The
+// accumulator O stays in TMEM for a unit's whole walk; the reference maximum m moves
+// only when it is 8 or more behind in log2 units (weights up to 2^8 keep their
+// relative precision), so O is seldom rescaled. Where the mask cuts a tile, the
+// keys that a row sees are bits, and only warps that have a hidden one apply them.
 //
 // Every wait is bounded; on expiry the kernel records RGLRU_ERR_TIMEOUT (wait
 // site 7), drains what it issued and returns.
@@ -32,7 +35,6 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 320;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSite = 7;
@@ -40,74 +42,160 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 
 template <int DH> struct Cfg {
+  static constexpr int kNQ = DH == 256 ? 1 : 2;          // query tiles of a block
+  static constexpr int kNS = DH == 256 ? 2 : 1;          // score buffers of a query tile
   static constexpr int kCols = DH < 128 ? DH : 128;      // columns of a slot
   static constexpr int kPer = DH / kCols;                // slots of a tile
   static constexpr int kSlotBytes = kBN * kCols * 2;
-  static constexpr int kSlots = DH == 256 ? 5 : DH == 128 ? 2 : 4;
-  static constexpr int kNS = DH == 256 ? 2 : 1;          // score buffers
-  static constexpr int kTmem = DH == 256 ? 512 : 256;
-  static constexpr int kQBytes = kBM * DH * 2;
-  static constexpr int kOffRing = kQBytes;
+  static constexpr int kSlots = DH == 64 ? 8 : 5;
+  static constexpr int kQBytes = kBM * DH * 2;           // of one query tile
+  static constexpr int kPoly = 4;                         // of 16 pairs of scores (weights32)
+  static constexpr int kG = kNQ == 2 ? 1 : 2;            // warp groups that share a tile's columns
+  static constexpr int kSoftmax = 8;                     // softmax warps
+  static constexpr int kThreads = (kSoftmax + 4) * 32;   // whole warp groups, for the register split
+  static constexpr int kOffRing = kNQ * kQBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-  static constexpr int kNumBars = 2 * kSlots + 1 + 2 * kNS + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + kNQ * (2 * kNS + 3) + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffMax = kOffMisc + 16;            // [2][2 groups][128 rows]
-  static constexpr int kSmem = kOffMax + 2 * 2 * kBM * 4;
-  static constexpr int kBlocks = DH == 256 ? 1 : 2;      // per SM
-  static constexpr bool kReread = kBlocks == 2;
+  static constexpr int kOffMax = kOffMisc + 16;          // [2][2 groups][128 rows]
+  static constexpr int kSmem = kOffMax + (kG == 2 ? 2 * 2 * kBM * 4 : 0);
+  static_assert(kSmem <= kMaxSmem && kNQ * (DH + kNS * kBN) <= 512, "shared memory, TMEM");
 };
-static_assert(Cfg<256>::kSmem <= kMaxSmem && 2 * (Cfg<128>::kSmem + 1024) <= 233472, "shared memory");
+
+// Scores whose bit is not set become -inf; nothing is done where all of a warp's are.
+__device__ __forceinline__ void hide(float (&v)[32], uint32_t bits) {
+  if (__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) return;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((bits >> e) & 1u)) v[e] = -INFINITY;
+}
+
+// The largest of N x 32 scores, in four chains.
+template <int N> __device__ __forceinline__ float max_of(const float (&v)[N][32]) {
+  float m[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) m[x] = fmaxf(v[0][2 * x], v[0][2 * x + 1]);
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int e = c == 0 ? 8 : 0; e < 32; e += 2) m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], v[c][e], v[c][e + 1]);
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// 32 scores of a row to weights 2^(v c - m), packed as bf16; sum gains them. kPoly
+// of the 16 pairs go by ex2_pair: the hardware's 2^x gives 16 results a cycle and
+// SM, as long for a tile of 128 x 128 scores as the tensor core needs for a 128-wide
+// head, while the FMA pipes have room.
+template <int kPoly>
+__device__ __forceinline__ void weights32(const float (&v)[32], unsigned long long cc,
+                                          unsigned long long mm, unsigned long long (&sum)[2],
+                                          uint32_t (&packed)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float a, b;
+    unpair(fma2(pair(v[2 * e], v[2 * e + 1]), cc, mm), a, b);
+    if ((e * kPoly) % 16 < kPoly) {                       // spread evenly
+      ex2_pair(a, b);
+    } else {
+      a = ex2(a);
+      b = ex2(b);
+    }
+    sum[e & 1] = add2(sum[e & 1], pair(a, b));
+    packed[e] = bf16x2(a, b);
+  }
+}
 
 struct Params {
   AttnArgs a;
-  int n_qt;      // query tiles
-  int v8;        // out rows may be stored 32 bytes at a time
-  float c;       // scale * log2 e
+  int n_qt;        // query tiles of a row; pairs of them when `rows2`
+  int n_h;         // heads of a row; pairs of them when a block's two tiles are two heads
+  int rows2;       // a block's two query tiles follow each other in one head
+  unsigned units;
+  int v8;          // out rows may be stored 32 bytes at a time
+  float c;         // scale * log2 e
 };
 
+// One unit of work: a block's query tiles (128 queries of one head each) and the
+// key tiles that any of them sees. Two tiles are two heads that share keys, or,
+// where heads are odd in a group, two tiles of one head. Heads fastest (they share
+// keys), then rows, then query tiles from the last (the longest walks of an
+// unwindowed causal mask come first).
+template <int NQ> struct Unit {
+  int h, b, q0, rows2;
+  RowLens n;
+  KeyTiles kt;
+  __device__ Unit(const Params &prm, unsigned u) {
+    const AttnArgs &p = prm.a;
+    rows2 = NQ == 2 ? prm.rows2 : 0;
+    h = static_cast<int>(u % static_cast<unsigned>(prm.n_h)) * (NQ == 2 && !rows2 ? 2 : 1);
+    const unsigned rest = u / static_cast<unsigned>(prm.n_h);
+    b = static_cast<int>(rest % static_cast<unsigned>(p.B));
+    q0 = (prm.n_qt - 1 - static_cast<int>(rest / static_cast<unsigned>(p.B))) * kBM * (1 + rows2);
+    n = row_lens(p, b);
+    kt = {0, 0, 0};
+    if (q0 < n.nq)
+      kt = key_tiles(q0 + p.S - p.T, min(q0 + kBM * (1 + rows2), n.nq) - 1 + p.S - p.T, n.nk, p.window,
+                     p.sinks, kBN);
+  }
+  __device__ int head(int q) const { return h + (NQ == 2 && !rows2 ? q : 0); }
+  __device__ int first(int q) const { return q0 + (NQ == 2 && rows2 ? q * kBM : 0); }
+  // whether any query of tile q sees any key of key tile i
+  __device__ bool sees(const AttnArgs &p, int q, int i) const {
+    if (NQ == 1 || !rows2) return true;
+    const int f = first(q), off = p.S - p.T, k0 = kt.tile(i) * kBN;
+    return f < n.nq && k0 <= min(f + kBM, n.nq) - 1 + off &&
+           (p.window == 0 || k0 + kBN - 1 > f + off - p.window || k0 < p.sinks);
+  }
+  // the last key tile that tile q sees, or -1
+  __device__ int last(const AttnArgs &p, int q) const {
+    if (NQ == 1 || !rows2) return kt.n - 1;
+    const int f = first(q), hi = min(min(f + kBM, n.nq) - 1 + p.S - p.T, n.nk - 1);
+    if (f >= n.nq || hi < 0) return -1;
+    const int x = hi / kBN;
+    return x < kt.win ? x : kt.sink_end + x - kt.win;
+  }
+};
+
+// The block's r-th unit: units come sorted by length, and every second round runs
+// backwards over the blocks, so that their sums stay close.
+__device__ __forceinline__ unsigned unit_at(unsigned r) {
+  return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+}
+
+// Ring fills of a unit in order of use: the K and V of tile i are fills
+// fill_of(i, is_v) .. + kPer - 1. One score buffer: K0 V0 K1 V1 ...; two: K0 K1 V0
+// K2 V1 ... K(n-1) V(n-2) V(n-1).
+template <int DH> __device__ __forceinline__ int fill_of(int i, bool is_v, int n) {
+  using C = Cfg<DH>;
+  if (C::kNS == 1) return (2 * i + (is_v ? 1 : 0)) * C::kPer;
+  if (!is_v) return (i == 0 ? 0 : 2 * i - 1) * C::kPer;
+  return (i + 1 < n ? 2 * i + 2 : 2 * i + 1) * C::kPer;
+}
+
 template <int DH>
-__global__ void __launch_bounds__(kThreads, Cfg<DH>::kBlocks)
+__global__ void __launch_bounds__(Cfg<DH>::kThreads, 1)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Params prm) {
   using C = Cfg<DH>;
+  using Un = Unit<C::kNQ>;
+  constexpr int kTma = C::kSoftmax, kMma = C::kSoftmax + 1;       // warps
   extern __shared__ __align__(1024) unsigned char sm[];
   const AttnArgs &p = prm.a;
   if ((smem_u32(sm) & 1023u) != 0u) {
     if (threadIdx.x == 0 && p.dev_status) atomicCAS(p.dev_status, 0, RGLRU_ERR_UNSUPPORTED);
     return;
   }
-  // heads fastest (they share keys), then rows, then query tiles from the last
-  // (the longest walks of an unwindowed causal mask start first)
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.Hq));
-  const unsigned rest = blockIdx.x / static_cast<unsigned>(p.Hq);
-  const int b = static_cast<int>(rest % static_cast<unsigned>(p.B));
-  const int q0 = (prm.n_qt - 1 - static_cast<int>(rest / static_cast<unsigned>(p.B))) * kBM;
-  const RowLens n = row_lens(p, b);
-  if (q0 >= n.nq) return;
-  const int off = p.S - p.T, kvh = h / (p.Hq / p.Hkv);
-  const int q_last = min(q0 + kBM, n.nq) - 1;
-  const KeyTiles kt = key_tiles(q0 + off, q_last + off, n.nk, p.window, p.sinks, kBN);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-  if (kt.n == 0) {                                       // no query of the tile sees a key
-    for (int i = tid; i < (q_last - q0 + 1) * (DH / 8); i += kThreads) {
-      const int t = q0 + i / (DH / 8);
-      reinterpret_cast<uint4 *>(out + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * DH)[i % (DH / 8)] =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (p.lse != nullptr)
-      for (int i = tid; i <= q_last - q0; i += kThreads)
-        p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + q0 + i] = -INFINITY;
-    return;
-  }
-
+  const int off = p.S - p.T;
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
   uint64_t *empty = full + C::kSlots;
-  uint64_t *q_full = empty + C::kSlots;
-  uint64_t *s_full = q_full + 1;
-  uint64_t *p_full = s_full + C::kNS;
-  uint64_t *o_done = p_full + C::kNS;
-  uint64_t *all_done = o_done + 1;                       // every MMA of the block
+  uint64_t *q_full = empty + C::kSlots, *q_empty = q_full + 1;
+  uint64_t *s_full = q_empty + 1;                        // [kNQ][kNS]
+  uint64_t *p_full = s_full + C::kNQ * C::kNS;           // [kNQ][kNS]
+  uint64_t *o_done = p_full + C::kNQ * C::kNS;           // [kNQ] a tile's P V
+  uint64_t *all_done = o_done + C::kNQ;                  // [kNQ] a unit's last P V
+  uint64_t *o_free = all_done + C::kNQ;                  // [kNQ] a unit's O was read
+  uint64_t *drained = o_free + C::kNQ;                   // used when a wait expired
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + C::kOffMisc + 4);
   if (tid == 0) {
@@ -116,24 +204,28 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
-    for (int s = 0; s < C::kNS; ++s) {
+    mbar_init(q_empty, 1);
+    mbar_init(drained, 1);
+    for (int s = 0; s < C::kNQ * C::kNS; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 8);
+      mbar_init(&p_full[s], 4 * C::kG);
     }
-    mbar_init(o_done, 1);
-    mbar_init(all_done, 1);
+    for (int q = 0; q < C::kNQ; ++q) {
+      mbar_init(&o_done[q], 1);
+      mbar_init(&all_done[q], 1);
+      mbar_init(&o_free[q], 4 * C::kG);
+    }
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, C::kTmem);
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t t_o = tmem, t_s = tmem + DH;            // O, then the score buffers
+  const uint32_t tmem = *tmem_slot;                      // O of each query tile, then the scores
   auto give_up = [&]() {
     if (!*abort) {
       if (p.dev_status) atomicCAS(p.dev_status, 0, RGLRU_ERR_TIMEOUT | (kSite << 8) |
@@ -142,63 +234,69 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
   };
 
-  // Slots in order of use: the K and V of tile i are fills at(i, is_v) ..+kPer-1.
-  // One score buffer: K0 V0 K1 V1 ...; two: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-  auto at = [&](int i, bool is_v) -> int {
-    if (C::kNS == 1) return (2 * i + (is_v ? 1 : 0)) * C::kPer;
-    if (!is_v) return (i == 0 ? 0 : 2 * i - 1) * C::kPer;
-    return (i + 1 < kt.n ? 2 * i + 2 : 2 * i + 1) * C::kPer;
-  };
-
-  if (warp == 8) {
+  // The block is launched with 168 registers a thread (12 warps); the copy and MMA
+  // warps give up some of theirs to the softmax warps: 8 x 208 + 4 x 88 = 12 x 168.
+  if (warp >= kTma) {
+  set_registers<-88>();
+  if (warp == kTma) {
     // ============================ TMA producer ============================
     if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, C::kQBytes);
-      for (int c = 0; c < DH / 64; ++c)
-        tma_load_4d(sm + c * (kBM * 128), &tmap_q, q_full, c * 64, q0, h, b);
-      const int fills = 2 * kt.n * C::kPer;
-      int f = 0;
-      // walk K and V in the order of `at`
-      int ik = 0, iv = 0;
-      while (f < fills) {
-        bool is_v;
-        int i;
-        if (ik < kt.n && at(ik, false) == f) {
-          is_v = false;
-          i = ik++;
-        } else {
-          is_v = true;
-          i = iv++;
-        }
-        bool ok = true;
-        for (int x = 0; x < C::kPer && ok; ++x, ++f) {
-          const int s = f % C::kSlots;
-          if (!mbar_wait(&empty[s], ((f / C::kSlots) & 1) ^ 1, abort, kWaitNs)) {
-            give_up();
-            ok = false;
-            break;
+      int f = 0, nu = 0;                                 // fills and units issued
+      bool ok = true;
+      for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
+        const Un un(prm, u);
+        if (un.kt.n == 0) continue;
+        const int kvh = un.h / (p.Hq / p.Hkv);
+        const int fills = 2 * un.kt.n * C::kPer;
+        // K and V tiles in the order of fill_of; Q after the first of them, which
+        // may come while the last unit still uses its Q
+        int ik = 0, iv = 0;
+        for (int g = 0; g < fills && ok;) {
+          const bool is_v = !(ik < un.kt.n && fill_of<DH>(ik, false, un.kt.n) == g);
+          const int i = is_v ? iv++ : ik++;
+          for (int x = 0; x < C::kPer && ok; ++x, ++g, ++f) {
+            const int s = f % C::kSlots;
+            if (!mbar_wait(&empty[s], ((f / C::kSlots) & 1) ^ 1, abort, kWaitNs)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[s], C::kSlotBytes);
+            for (int c = 0; c < C::kCols / 64; ++c)
+              tma_load_4d(sm + C::kOffRing + s * C::kSlotBytes + c * (kBN * 128), is_v ? &tmap_v : &tmap_k,
+                          &full[s], x * C::kCols + c * 64, un.kt.tile(i) * kBN, kvh, un.b);
           }
-          mbar_arrive_expect_tx(&full[s], C::kSlotBytes);
-          for (int c = 0; c < C::kCols / 64; ++c)
-            tma_load_4d(sm + C::kOffRing + s * C::kSlotBytes + c * (kBN * 128),
-                        is_v ? &tmap_v : &tmap_k, &full[s], x * C::kCols + c * 64, kt.tile(i) * kBN,
-                        kvh, b);
+          if (ok && !is_v && i == 0) {
+            if (!mbar_wait(q_empty, (nu & 1) ^ 1, abort, kWaitNs)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(q_full, C::kNQ * C::kQBytes);
+            for (int q = 0; q < C::kNQ; ++q)
+              for (int c = 0; c < DH / 64; ++c)
+                tma_load_4d(sm + q * C::kQBytes + c * (kBM * 128), &tmap_q, q_full, c * 64, un.first(q),
+                            un.head(q), un.b);
+            ++nu;
+          }
         }
-        if (!ok) break;
       }
       if (*abort) {
-        mbar_wait_drain(q_full, 0, kDrainNs);
+        if (nu > 0) mbar_wait_drain(q_full, (nu - 1) & 1, kDrainNs);
         for (int j = f - 1; j >= 0 && j >= f - C::kSlots; --j)
           mbar_wait_drain(&full[j % C::kSlots], (j / C::kSlots) & 1, kDrainNs);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kMma) {
     // ============================= MMA issuer =============================
     // The whole warp walks, one elected lane issues.
     constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
     constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
     const uint32_t base = smem_u32(sm);
     bool ok = true;
+    int f0 = 0;                                          // fills before this unit
+    int units = 0;                                       // units before this one
+    int js[2] = {0, 0}, jp[2] = {0, 0}, nu[2] = {0, 0};  // tiles scored, tiles added, units, by query tile
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
         give_up();
@@ -207,13 +305,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) tc_fence_after();
       return ok;
     };
-    auto scores = [&](int i) {
-      const int f0 = at(i, false);
-      const uint32_t d = t_s + (i % C::kNS) * kBN;
+    // S of query tile q and key tile i; `last`: the tile's K has no later reader
+    auto scores = [&](const Un &un, int q, int i, bool last) {
+      const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[q] % C::kNS;
+      const uint32_t d = tmem + C::kNQ * DH + sb * kBN;
       for (int x = 0; x < C::kPer; ++x) {
-        const int s = (f0 + x) % C::kSlots;
-        if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
-        const uint32_t ad = desc_lo(base + x * (C::kCols / 64) * (kBM * 128), 16);
+        const int s = (f + x) % C::kSlots;
+        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
+        const uint32_t ad = desc_lo(base + q * C::kQBytes + x * (C::kCols / 64) * (kBM * 128), 16);
         const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, 16);
         if (elect_one()) {
 #pragma unroll
@@ -223,49 +322,96 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const uint32_t o = ((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4;
             mma_ss(d, ad + o, bd + o, id_s, k > 0 ? 1u : x > 0);
           }
-          mma_commit(&empty[s]);
-          if (x == C::kPer - 1) mma_commit(&s_full[i % C::kNS]);
+          if (last) mma_commit(&empty[s]);
+          if (x == C::kPer - 1) {
+            mma_commit(&s_full[sb]);
+            if (last && i == un.kt.n - 1) mma_commit(q_empty);
+          }
         }
         __syncwarp();
       }
+      ++js[q];
     };
-    auto values = [&](int i) {
-      if (!wait(&p_full[i % C::kNS], (i / C::kNS) & 1)) return;
-      const int f0 = at(i, true);
-      const uint32_t a = t_s + (i % C::kNS) * kBN;
+    // O of query tile q gains P V of key tile i; `first`, `done`: of the unit
+    auto values = [&](const Un &un, int q, int i, bool first, bool done, bool last) {
+      const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[q] % C::kNS;
+      if (!wait(&p_full[sb], (jp[q] / C::kNS) & 1)) return;
+      if (first && nu[q] > 0 && !wait(&o_free[q], (nu[q] - 1) & 1)) return;
+      const uint32_t a = tmem + C::kNQ * DH + sb * kBN;
       for (int x = 0; x < C::kPer; ++x) {
-        const int s = (f0 + x) % C::kSlots;
-        if (!wait(&full[s], ((f0 + x) / C::kSlots) & 1)) return;
+        const int s = (f + x) % C::kSlots;
+        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
         const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBN / 16; ++k)
-            mma_ts(t_o + x * C::kCols, a + (k >> 2) * 64 + (k & 3) * 8, bd + ((k * 16 * 128) >> 4), id_o, k > 0 ? 1u : i > 0);
-          mma_commit(&empty[s]);
-          if (x == C::kPer - 1) mma_commit(o_done);
+            mma_ts(tmem + q * DH + x * C::kCols, a + (C::kG == 2 ? (k >> 2) * 64 + (k & 3) * 8 : k * 8), bd + ((k * 16 * 128) >> 4),
+                   id_o, k > 0 ? 1u : !first);
+          if (last) mma_commit(&empty[s]);
+          if (x == C::kPer - 1) {
+            mma_commit(&o_done[q]);
+            if (done) mma_commit(&all_done[q]);
+          }
         }
         __syncwarp();
       }
+      ++jp[q];
     };
-    wait(q_full, 0);
-    if (ok) scores(0);
-    for (int i = 0; i < kt.n && ok; ++i) {
-      if (C::kNS == 2 && i + 1 < kt.n) scores(i + 1);
-      if (ok) values(i);
-      if (C::kNS == 1 && ok && i + 1 < kt.n) scores(i + 1);
+    for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
+      const Un un(prm, u);
+      const int n = un.kt.n;
+      if (n == 0) continue;
+      wait(q_full, units & 1);
+      ++units;
+      if constexpr (C::kNQ == 1) {
+        if (ok) scores(un, 0, 0, true);
+        for (int i = 0; i < n && ok; ++i) {
+          if (i + 1 < n) scores(un, 0, i + 1, true);
+          if (ok) values(un, 0, i, i == 0, i == n - 1, true);
+        }
+        ++nu[0];
+      } else {
+        // the two query tiles take turns: while the softmax works on one's scores,
+        // the other's P V and next S run. A tile of one that sees none of the keys
+        // is passed over; its part in releasing the slots falls to the other.
+        const int end[2] = {un.last(p, 0), un.last(p, 1)};
+        bool begun[2] = {false, false};
+        for (int i = -1; i < n && ok; ++i) {
+          const bool now1 = i >= 0 && un.sees(p, 1, i), next1 = i + 1 < n && un.sees(p, 1, i + 1);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (ok && (q == 1 ? now1 : i >= 0 && un.sees(p, 0, i))) {
+              values(un, q, i, !begun[q], i == end[q], q == 1 || !now1);
+              begun[q] = true;
+            }
+            if (ok && (q == 1 ? next1 : i + 1 < n && un.sees(p, 0, i + 1)))
+              scores(un, q, i + 1, q == 1 || !next1);
+          }
+        }
+        nu[0] += begun[0] ? 1 : 0;
+        nu[1] += begun[1] ? 1 : 0;
+      }
+      f0 += 2 * n * C::kPer;
     }
-    if (elect_one()) mma_commit(all_done);
-    if (*abort) mbar_wait_drain(all_done, 0, kDrainNs);
+    if (*abort) {                                        // let what was issued finish
+      if (elect_one()) mma_commit(drained);
+      mbar_wait_drain(drained, 0, kDrainNs);
+    }
+  }
   } else {
+    set_registers<208>();
     // =============================== softmax ==============================
-    // Warp group g: columns 64 g .. of a tile. Thread = row = TMEM lane.
-    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    // Thread = row = TMEM lane, and kCols of a key tile's columns: all 128, or, one
+    // query tile a block, half of them (warp group g).
+    constexpr int kCols = kBN / C::kG, kOut = DH / C::kG;
+    const int q = C::kNQ == 2 ? warp >> 2 : 0, g = C::kG == 2 ? warp >> 2 : 0, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int pos = q0 + row + off;
-    const DeadKeys dead = dead_keys(p, n.nk);
+    const uint32_t t_o = tmem + lanes + q * DH + g * kOut;
+    const uint32_t t_s = tmem + lanes + C::kNQ * DH + q * C::kNS * kBN + g * kCols;
     float *shared_max = reinterpret_cast<float *>(sm + C::kOffMax);
-    float m = -INFINITY, l = 0.0f;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
     bool ok = true;                  // a warp whose wait expired still meets the block barriers
+    int f0 = 0, j = 0, nu = 0;       // fills before this unit; tiles so far; units
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
         give_up();
@@ -274,146 +420,180 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) tc_fence_after();
       return ok;
     };
-    for (int i = 0; i < kt.n; ++i) {
-      const int s = i % C::kNS, k0 = kt.tile(i) * kBN;
-      const uint32_t ts = t_s + s * kBN + g * 64 + lanes;
-      // whether every query of the tile sees every key of the tile
-      const bool whole = k0 + kBN - 1 <= min(q0 + off, n.nk - 1) &&
-                         (p.window == 0 || k0 > q0 + kBM - 1 + off - p.window || k0 + kBN <= p.sinks);
-      const int hi = min(pos, n.nk - 1) - k0;
-      const int lo = p.window > 0 ? pos - p.window + 1 - k0 : -1, sk = p.sinks - k0;
-      auto mask = [&](float (&v)[32], int c) {
-        if (whole) return;
+    // the other group's value for this row; buffers alternate from call to call
+    auto exchange = [&](float x, int buffer) -> float {
+      shared_max[(buffer * 2 + g) * kBM + row] = x;
+      bar_sync_group(0);
+      return shared_max[(buffer * 2 + (g ^ 1)) * kBM + row];
+    };
+    for (unsigned r = 0, u; (u = unit_at(r)) < prm.units; ++r) {
+      const Un un(prm, u);
+      const int q0 = un.first(q), t = q0 + row;
+      const long long out_row = (static_cast<long long>(un.b) * p.T + t) * p.Hq + un.head(q);
+      const long long lse_row = (static_cast<long long>(un.b) * p.Hq + un.head(q)) * p.T + t;
+      float m = -INFINITY, l = 0.0f;
+      bool begun = false;
+      for (int i = 0; i < un.kt.n; ++i) {
+        if (!un.sees(p, q, i)) continue;
+        const bool first = !begun;
+        begun = true;
+        const int s = j % C::kNS, k0 = un.kt.tile(i) * kBN;
+        const uint32_t ts = t_s + s * kBN;
+        // Where every query of the tile sees every key of it, the scores stay in
+        // registers from the maximum to the weights. Elsewhere they are read twice, 32
+        // columns at a time in rolled loops (unrolled over a row, that path alone
+        // outran the instruction cache: 7000 cycles a tile), with the keys that this
+        // row sees of 32 as bits.
+        const bool whole = k0 + kBN - 1 <= min(q0 + off, un.n.nk - 1) &&
+                           (p.window == 0 || k0 > q0 + kBM - 1 + off - p.window || k0 + kBN <= p.sinks);
+        auto seen = [&](int c) -> uint32_t {
+          const int key = k0 + g * kCols + c, hi = min(t + off, un.n.nk - 1) - key;
+          const int lo = p.window > 0 ? t + off - p.window + 1 - key : 0;
+          return bits_between(lo, hi) | bits_between(0, min(hi, p.sinks - key - 1));
+        };
+        float v[kCols / 32][32], top = -INFINITY;
+        if (wait(&s_full[q * C::kNS + s], (j / C::kNS) & 1)) {
+          if (whole) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int j = g * 64 + c * 32 + e;
-          if (!(j <= hi && (j >= lo || j < sk))) v[e] = -INFINITY;
-        }
-      };
-      float v[2][32], mx[2] = {-INFINITY, -INFINITY};
-      if (wait(&s_full[s], (i / C::kNS) & 1)) {
-        // two blocks an SM leave a thread under 102 registers: the scores are read
-        // 32 at a time, once for the maximum and once for the weights
-        if constexpr (!C::kReread) {
-          tmem_ld32(ts, v[0]);
-          tmem_ld32(ts + 32, v[1]);
-          tmem_wait_ld32(v[0]);
-          tmem_wait_ld32(v[1]);
-        }
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + c * 32, v[c]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float(&u)[32] = v[C::kReread ? 0 : x];
-          if constexpr (C::kReread) {
-            tmem_ld32(ts + x * 32, u);
-            tmem_wait_ld32(u);
-          }
-          mask(u, x);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx[x] = max3(mx[x], u[e], u[e + 1]);
-        }
-      }
-      const float mine = fmaxf(mx[0], mx[1]);
-      shared_max[((i & 1) * 2 + g) * kBM + row] = mine;
-      bar_sync_softmax();
-      if (!ok) continue;
-      const float top = fmaxf(mine, shared_max[((i & 1) * 2 + (g ^ 1)) * kBM + row]) * prm.c;
-      const bool grow = top > m + kSlack || m == -INFINITY;
-      const float mn = grow ? fmaxf(top, m) : m;
-      if (__any_sync(0xFFFFFFFFu, mn != m)) {
-        const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
-        l *= f;
-        m = mn;
-        if (i > 0 && wait(o_done, (i - 1) & 1)) {        // O so far: P V of the last tile is done
+            for (int c = 0; c < kCols / 32; ++c) tmem_wait_ld32(v[c]);
+            top = max_of(v);
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < DH / 64; ++c) {
-            const uint32_t to = t_o + lanes + g * (DH / 2) + c * 32;
-            float o[32];
-            tmem_ld32(to, o);
-            tmem_wait_ld32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(to, o);
+            for (int c = 0; c < kCols; c += 32) {
+              float w[1][32];
+              tmem_ld32(ts + c, w[0]);
+              const uint32_t bits = seen(c);
+              tmem_wait_ld32(w[0]);
+              hide(w[0], bits);
+              top = fmaxf(top, max_of(w));
+            }
           }
-          tmem_wait_st();
         }
-        if (!ok) continue;
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-base, -base);
-      unsigned long long sum[2] = {0ull, 0ull};
-      // the weights of this group's columns go to the first half of its score columns
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float(&u)[32] = v[C::kReread ? 0 : c];
-        if constexpr (C::kReread) {
-          tmem_ld32(ts + c * 32, u);
-          tmem_wait_ld32(u);
-          mask(u, c);
+        if constexpr (C::kG == 2) top = fmaxf(top, exchange(top, j & 1));
+        if (!ok) {
+          ++j;
+          continue;
         }
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float a, bb;
-          unpair(fma2(pair(u[e], u[e + 1]), cc, mm), a, bb);
-          a = ex2(a);
-          bb = ex2(bb);
-          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, bb));
-          w[e / 2] = bf16x2(a, bb);
-        }
-        tmem_st16u(ts + c * 16, w);
-      }
-      float s0, s1;
-      unpair(add2(sum[0], sum[1]), s0, s1);
-      l += s0 + s1;
-      if (dead.any(k0, kBN)) {
-        // zero the value rows that no query sees, once V is there
-        const int f0 = at(i, true);
-        for (int x = 0; x < C::kPer; ++x) {
-          const int sl = (f0 + x) % C::kSlots;
-          if (wait(&full[sl], ((f0 + x) / C::kSlots) & 1) && g == 0 && dead.in(k0 + row))
-            for (int c = 0; c < C::kCols / 64; ++c)
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4 *>(sm + C::kOffRing + sl * C::kSlotBytes + c * (kBN * 128) +
-                                           row * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
-    }
-    // the row's sum, from both groups
-    shared_max[((kt.n & 1) * 2 + g) * kBM + row] = l;
-    bar_sync_softmax();
-    l += shared_max[((kt.n & 1) * 2 + (g ^ 1)) * kBM + row];
-    if (wait(all_done, 0)) {
-      const int t = q0 + row;
-      const bool live = t < n.nq;
-      const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-      __nv_bfloat16 *dst = out + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * DH + g * (DH / 2);
+        top *= prm.c;
+        const bool grow = top > m + kSlack || m == -INFINITY;
+        const float mn = grow ? fmaxf(top, m) : m;
+        if (__any_sync(0xFFFFFFFFu, mn != m)) {
+          const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
+          l *= f;
+          m = mn;
+          if (!first && wait(&o_done[q], (j - 1) & 1)) {  // O so far: P V of the last tile is done
 #pragma unroll 1
-      for (int c = 0; c < DH / 64; ++c) {
-        float o[32];
-        tmem_ld32(t_o + lanes + g * (DH / 2) + c * 32, o);
-        tmem_wait_ld32(o);
+            for (int c = 0; c < kOut; c += 32) {
+              float o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(t_o + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-base, -base);
+        unsigned long long sum[2] = {0ull, 0ull};
+        // the weights of a group's columns go to the first half of its score columns
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t packed[16];
+            weights32<C::kPoly>(v[c], cc, mm, sum, packed);
+            tmem_st16u(ts + c * 16, packed);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += 32) {
+            float w[32];
+            tmem_ld32(ts + c, w);
+            const uint32_t bits = seen(c);
+            tmem_wait_ld32(w);
+            hide(w, bits);
+            uint32_t packed[16];
+            weights32<C::kPoly>(w, cc, mm, sum, packed);
+            tmem_st16u(ts + c / 2, packed);
+          }
+        }
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        const DeadKeys dead = dead_keys(p, un.n.nk);
+        if (dead.any(k0, kBN)) {
+          // zero the value rows that no query sees, once V is there (each query tile
+          // does, before its own product: zeros over zeros)
+          const int f = f0 + fill_of<DH>(i, true, un.kt.n);
+          for (int x = 0; x < C::kPer; ++x) {
+            const int sl = (f + x) % C::kSlots;
+            if (wait(&full[sl], ((f + x) / C::kSlots) & 1) && g == 0 && dead.in(k0 + row))
+              for (int c = 0; c < C::kCols / 64; ++c)
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<uint4 *>(sm + C::kOffRing + sl * C::kSlotBytes + c * (kBN * 128) +
+                                             row * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&p_full[q * C::kNS + s]);
+        ++j;
+      }
+      f0 += 2 * un.kt.n * C::kPer;
+      const bool live = t < un.n.nq;
+      if (!begun) {                                      // sees no key
         if (live) {
-          if (m == -INFINITY) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-          }
-          store_row32(dst + c * 32, o, inv, prm.v8 != 0);
+          for (int e = 0; e < kOut / 8; ++e)
+            reinterpret_cast<uint4 *>(out + out_row * DH + g * kOut)[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (g == 0 && p.lse != nullptr) p.lse[lse_row] = -INFINITY;
         }
+        continue;
       }
-      if (live && g == 0 && p.lse != nullptr)
-        p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] =
-            m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+      if constexpr (C::kG == 2) {
+        l += exchange(l, j & 1);                         // the row's sum, from both groups
+        bar_sync_group(0);                               // the next unit's first tile writes there
+      }
+      if (wait(&all_done[q], nu & 1)) {
+        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        __nv_bfloat16 *dst = out + out_row * DH + g * kOut;
+#pragma unroll 1
+        for (int c = 0; c < kOut; c += 64) {
+          float o[2][32];
+          tmem_ld32(t_o + c, o[0]);
+          tmem_ld32(t_o + c + 32, o[1]);
+          tmem_wait_ld32(o[0]);
+          tmem_wait_ld32(o[1]);
+          if (c + 64 == kOut) {                          // O may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[q]);
+          }
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (m == -INFINITY) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[x][e] = 0.0f;
+              }
+              store_row32(dst + c + x * 32, o[x], inv, prm.v8 != 0);
+            }
+          }
+        }
+        if (live && g == 0 && p.lse != nullptr)
+          p.lse[lse_row] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+      }
+      ++nu;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, C::kTmem);
+  if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
 template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
@@ -427,11 +607,13 @@ template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   Params prm;
   prm.a = p;
-  prm.n_qt = ceil_div(p.T, kBM);
+  prm.rows2 = C::kNQ == 2 && (p.Hq / p.Hkv) % 2 != 0 ? 1 : 0;
+  prm.n_qt = ceil_div(p.T, kBM * (1 + prm.rows2));
+  prm.n_h = C::kNQ == 2 && !prm.rows2 ? p.Hq / 2 : p.Hq;
+  prm.units = static_cast<unsigned>(static_cast<long long>(prm.n_qt) * p.B * prm.n_h);
   prm.v8 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 ? 1 : 0;
   prm.c = p.scale * kLog2e;
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(prm.n_qt) * p.B * p.Hq);
-  attn_fwd_tc_kernel<DH><<<grid, kThreads, C::kSmem, st>>>(mq, mk, mv, prm);
+  attn_fwd_tc_kernel<DH><<<prm.units < 148u ? prm.units : 148u, C::kThreads, C::kSmem, st>>>(mq, mk, mv, prm);
   return cudaGetLastError();
 }
 
