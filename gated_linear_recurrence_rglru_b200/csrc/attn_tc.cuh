@@ -200,6 +200,14 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   return upto & from;
 }
 
+// What has no bit set becomes `to`; nothing is done where all of a warp's have.
+__device__ __forceinline__ void hide(float (&v)[32], uint32_t bits, float to) {
+  if (__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) return;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((bits >> e) & 1u)) v[e] = to;
+}
+
 // Keys that no query of the call sees: [sinks, dead_lo) and [nk, S). Their rows
 // may hold anything, so a tile's rows among them are zeroed in shared memory
 // (weight 0 times NaN would be NaN).

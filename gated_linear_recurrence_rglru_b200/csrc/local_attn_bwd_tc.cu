@@ -324,20 +324,33 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         ok = false;
       }
       // (an expired wait: every thread still walks the block barriers)
-      // columns [lo, hi) or, for query rows, below sk are seen by this row
-      int lo, hi, sk = 0;
+      // the columns that this row sees, as bits of 32; all of them where the whole
+      // tile is seen by every row
       bool all;
-      if (kKeys) {
-        lo = r - off - t0;
-        hi = p.window > 0 && r >= p.sinks ? min(nq - t0, lo + p.window) : nq - t0;
+      uint32_t bits[kHalf / 32], ds_bits[kHalf / 32];      // and those whose scores have a gradient
+      if (kKeys)
         all = t0 + kBN <= nq && t0 + off >= wk.r0 + kBM - 1 &&
               (p.window == 0 || wk.r0 + kBM <= p.sinks || t0 + kBN - 1 + off < wk.r0 + p.window);
-      } else {
-        hi = min(r + off, nk - 1) + 1 - t0;
-        lo = p.window > 0 ? r + off - p.window + 1 - t0 : 0;
-        sk = p.sinks - t0;
+      else
         all = t0 + kBN - 1 <= min(wk.r0 + off, nk - 1) &&
               (p.window == 0 || t0 > wk.r0 + kBM - 1 + off - p.window || t0 + kBN <= p.sinks);
+#pragma unroll
+      for (int c = 0; c < kHalf / 32; ++c) {
+        bits[c] = ds_bits[c] = 0xFFFFFFFFu;
+        if (all) continue;
+        const int t1 = t0 + g * kHalf + c * 32;            // the first column's query or key
+        if (kKeys) {
+          const int lo = r - off - t1;
+          const int hi = (p.window > 0 && r >= p.sinks ? min(nq - t1, lo + p.window) : nq - t1) - 1;
+          bits[c] = bits_between(lo, hi);
+          // a query that sees one key: the one at position 0, or all of a window of one
+          ds_bits[c] = p.window == 1 && p.sinks == 0 ? 0u : bits[c] & ~bits_between(-off - t1, -off - t1);
+        } else {
+          const int hi = min(r + off, nk - 1) - t1;
+          bits[c] = bits_between(p.window > 0 ? r + off - p.window + 1 - t1 : 0, hi) |
+                    bits_between(0, min(hi, p.sinks - t1 - 1));
+          ds_bits[c] = attn_lone(r + off, p.window, p.sinks) ? 0u : bits[c];
+        }
       }
       const float *ls = stat + (i & 1) * 2 * kBN + g * kHalf;
       const uint32_t ts = tmem + lanes + C::kTS + sb * kBN + g * kHalf;
@@ -368,13 +381,8 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[c + e] = ex2(v[c + e]);
         }
-        if (!all) {
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) {
-            const int j = g * kHalf + c;
-            if (!(j < hi && (j >= lo || j < sk))) v[c] = 0.0f;
-          }
-        }
+        for (int c = 0; c < kHalf; c += 32) hide(*reinterpret_cast<float (*)[32]>(v + c), bits[c / 32], 0.0f);
         // walked rows that nobody sees, zeroed before a product reads them
         bool dead = false;
         if (kKeys)
@@ -415,11 +423,6 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           if (lane == 0) mbar_arrive(&p_full[sb]);
         }
       }
-      if (kFirst && !all) {                                // queries that see one key: dS = 0
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c)
-          if (attn_lone(kKeys ? t0 + g * kHalf + c + off : r + off, p.window, p.sinks)) v[c] = 0.0f;
-      }
       if (kFirst && ok) {
         if (!mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
           give_up();
@@ -433,7 +436,6 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
             float d[32];
             tmem_ld32(td + c, d);
             tmem_wait_ld32(d);
-            uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               unsigned long long d0 = dd, d1 = dd;
@@ -442,20 +444,14 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
                 d0 = pair(-x.x, -x.y);
                 d1 = pair(-x.z, -x.w);
               }
-              float a, bb;
-              unpair(mul2(add2(pair(d[e], d[e + 1]), d0), pair(v[c + e], v[c + e + 1])), a, bb);
-              if (!all) {                                  // hidden: 0, whatever dP holds
-                if (v[c + e] == 0.0f) a = 0.0f;
-                if (v[c + e + 1] == 0.0f) bb = 0.0f;
-              }
-              w[e / 2] = bf16x2(a, bb);
-              unpair(mul2(add2(pair(d[e + 2], d[e + 3]), d1), pair(v[c + e + 2], v[c + e + 3])), a, bb);
-              if (!all) {
-                if (v[c + e + 2] == 0.0f) a = 0.0f;
-                if (v[c + e + 3] == 0.0f) bb = 0.0f;
-              }
-              w[e / 2 + 1] = bf16x2(a, bb);
+              unpair(mul2(add2(pair(d[e], d[e + 1]), d0), pair(v[c + e], v[c + e + 1])), d[e], d[e + 1]);
+              unpair(mul2(add2(pair(d[e + 2], d[e + 3]), d1), pair(v[c + e + 2], v[c + e + 3])), d[e + 2],
+                     d[e + 3]);
             }
+            hide(d, ds_bits[c / 32], 0.0f);                // whatever dP holds there
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = bf16x2(d[2 * e], d[2 * e + 1]);
             tmem_st16u(td + c / 2, w);
           }
           tmem_wait_st();
