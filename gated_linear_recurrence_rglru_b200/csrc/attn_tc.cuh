@@ -81,9 +81,14 @@ template <int N> __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(-N));
 }
 
-// The 256 threads of one of two groups of eight warps meet.
-__device__ __forceinline__ void bar_sync_group(int group) {
-  asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory");
+// N threads of the softmax warps meet.
+template <int N> __device__ __forceinline__ void bar_sync_softmax() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // 16 consecutive TMEM columns of this thread's lane, as raw words.
@@ -107,6 +112,38 @@ __device__ __forceinline__ void tmem_wait_ld32(float (&v)[32]) {
                  "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                  "+f"(v[30]), "+f"(v[31])
                :
+               : "memory");
+}
+
+// The same for 32 or 16 columns: load, wait, and store of their bf16 pairs.
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[32]) {
+  tmem_ld32(t, v);
+  tmem_wait_ld32(v);
+}
+__device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[16]) {
+  tmem_ld16(t, v);
+  tmem_wait_ld16(v);
+}
+__device__ __forceinline__ void st_bf16(uint32_t t, const float (&v)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = bf16x2(v[2 * e], v[2 * e + 1]);
+  tmem_st16u(t, w);
+}
+__device__ __forceinline__ void st_bf16(uint32_t t, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = bf16x2(v[2 * e], v[2 * e + 1]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
@@ -169,26 +206,22 @@ __device__ __forceinline__ void ex2_pair(float &a, float &b) {
   b = __int_as_float(__float_as_int(rb) + (__float_as_int(zb) << 23));
 }
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// 32 floats as 32 bf16 (64 bytes) at dst; v8: dst is 32-byte aligned.
-__device__ __forceinline__ void store_row32(__nv_bfloat16 *dst, const float (&v)[32], float f, bool v8) {
-  uint32_t w[16];
+// N floats as bf16 (2 N bytes) at dst; v8: dst is 32-byte aligned.
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const float (&v)[N], float f, bool v8) {
+  uint32_t w[N / 2];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = bf16x2(v[2 * e] * f, v[2 * e + 1] * f);
+  for (int e = 0; e < N / 2; ++e) w[e] = bf16x2(v[2 * e] * f, v[2 * e + 1] * f);
   if (v8) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < N / 16; ++q)
       asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + q * 16),
                    "r"(w[8 * q]), "r"(w[8 * q + 1]), "r"(w[8 * q + 2]), "r"(w[8 * q + 3]),
                    "r"(w[8 * q + 4]), "r"(w[8 * q + 5]), "r"(w[8 * q + 6]), "r"(w[8 * q + 7])
                    : "memory");
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < N / 8; ++q)
       reinterpret_cast<uint4 *>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   }
 }
@@ -201,10 +234,10 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
 }
 
 // What has no bit set becomes `to`; nothing is done where all of a warp's have.
-__device__ __forceinline__ void hide(float (&v)[32], uint32_t bits, float to) {
+template <int N> __device__ __forceinline__ void hide(float (&v)[N], uint32_t bits, float to) {
   if (__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) return;
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
+  for (int e = 0; e < N; ++e)
     if (!((bits >> e) & 1u)) v[e] = to;
 }
 

@@ -18,10 +18,10 @@
 // Seven products (eight for 256-wide heads) instead of the five of one pass that
 // adds dQ up in memory by atomics, whose order would change the result.
 //
-// Warps 0-7 turn scores into weights, warp group g half of a tile's columns,
+// Warps 0-15 turn scores into weights, warp group g a quarter of a tile's columns,
 // thread = row = TMEM lane; P and dS go back to TMEM as bf16 over the scores
-// they came from and are the A operand of their product. Warp 8 issues the TMA
-// copies, warp 9 the MMAs in an order that keeps the tensor core fed: the next
+// they came from and are the A operand of their product. Warp 16 issues the TMA
+// copies, warp 17 the MMAs in an order that keeps the tensor core fed: the next
 // tile's S runs while dS is formed, and P of the next tile is formed during
 // `first` and dP.
 //
@@ -38,7 +38,8 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128;
-constexpr int kThreads = 320;
+constexpr int kWarps = 16;                             // weight warps; then copies, then MMAs
+constexpr int kThreads = (kWarps + 2) * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSite = 8;
@@ -84,6 +85,13 @@ template <int DH> constexpr int smem_bytes() {
     return Cfg<DH, true, true>::kSmem;
 }
 
+// A load that stays where it is written: issued now, used a step later.
+__device__ __forceinline__ float ld_early(const float *p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // Where a block stands: its rows, and the walk over the other side.
 struct Walk {
   int b, h, kvh;       // h: query rows only
@@ -95,24 +103,39 @@ struct Walk {
   int first;
 };
 
-// A step's head (key rows), and the first row of its tile.
-template <bool kKeys, int kBN> __device__ __forceinline__ void step_at(const Walk &w, int G, int i, int &h, int &t0) {
-  if (kKeys) {
-    const int x = w.first + i;
-    h = w.kvh * G + x / w.st.nq;
-    t0 = (w.st.q0 + x % w.st.nq) * kBN;
-  } else {
-    h = w.kvh;
-    t0 = w.kt.tile(i) * kBN;
+// The walk's place: a step's head (key rows), and the first row of its tile; moved
+// on without divisions.
+template <bool kKeys, int kBN> struct Step {
+  int i, h, t0;
+  __device__ Step(const Walk &w, int G) : i(0), h(w.kvh * G), t0(0) {
+    if (kKeys) {
+      h += w.first / w.st.nq;
+      t0 = (w.st.q0 + w.first % w.st.nq) * kBN;
+    } else {
+      h = w.kvh;
+      t0 = w.kt.tile(0) * kBN;
+    }
   }
-}
+  __device__ void next(const Walk &w) {
+    ++i;
+    if (kKeys) {
+      t0 += kBN;
+      if (t0 == (w.st.q0 + w.st.nq) * kBN) {
+        t0 = w.st.q0 * kBN;
+        ++h;
+      }
+    } else {
+      t0 = w.kt.tile(i) * kBN;
+    }
+  }
+};
 
 template <int DH, bool kKeys, bool kFirst, bool kSecond>
 __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, const CUtensorMap *my,
                                      const CUtensorMap *mu, const CUtensorMap *mw, const Walk &wk,
                                      bool whole_tile, size_t slot, unsigned char *sm) {
   using C = Cfg<DH, kFirst, kSecond>;
-  constexpr int kBN = C::kBN, kHalf = kBN / 2;
+  constexpr int kBN = C::kBN, kW = kBN / 4;             // columns of a warp group
   const AttnArgs &p = prm.a;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int G = p.Hq / p.Hkv, off = p.S - p.T;
@@ -134,15 +157,15 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       mbar_init(&w_full[s], 1);
       mbar_init(&w_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 8);
+      mbar_init(&p_full[s], kWarps);
     }
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kWarps);
     mbar_init(done, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -158,7 +181,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
     }
   };
 
-  if (warp == 8) {
+  if (warp == kWarps) {
     // ============================ TMA producer ============================
     if (lane == 0) {
       const int xh = kKeys ? wk.kvh : wk.h;
@@ -167,10 +190,9 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         tma_load_4d(sm + c * (kBM * 128), mx, x_full, c * 64, wk.r0, xh, wk.b);
         if (kFirst) tma_load_4d(sm + C::kOffY + c * (kBM * 128), my, x_full, c * 64, wk.r0, xh, wk.b);
       }
-      int i = 0, w_issued = 0, u_issued = 0;
-      for (; i < wk.n; ++i) {
-        int h, t0;
-        step_at<kKeys, kBN>(wk, G, i, h, t0);
+      int w_issued = 0, u_issued = 0;
+      for (Step<kKeys, kBN> st(wk, G); st.i < wk.n; st.next(wk)) {
+        const int i = st.i, h = st.h, t0 = st.t0;
         const int u = i & 1, w = i % C::kNW;
         if (!mbar_wait(&u_empty[u], ((i >> 1) & 1) ^ 1, abort, kWaitNs)) {
           give_up();
@@ -197,7 +219,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           mbar_wait_drain(&w_full[j % C::kNW], (j / C::kNW) & 1, kDrainNs);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kWarps + 1) {
     // ============================= MMA issuer =============================
     // The whole warp walks, one elected lane issues.
     constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
@@ -226,7 +248,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       const uint32_t bd = desc_lo(base + tile, kBN * 128);
 #pragma unroll
       for (int k = 0; k < kBN / 16; ++k)
-        mma_ts(d, a + (k / (kHalf / 16)) * kHalf + (k % (kHalf / 16)) * 8, bd + ((k * 16 * 128) >> 4),
+        mma_ts(d, a + (k / (kW / 16)) * kW + (k % (kW / 16)) * 8, bd + ((k * 16 * 128) >> 4),
                id_o, k > 0 ? 1u : add);
     };
     auto u_at = [&](int i) { return static_cast<uint32_t>(C::kOffU + (i & 1) * C::kTile); };
@@ -283,6 +305,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
     if (*abort) mbar_wait_drain(done, 0, kDrainNs);
   } else {
     // =============================== weights ==============================
+    // Thread = row = TMEM lane, warp group g the columns kW g .. of a tile.
     const int g = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int r = wk.r0 + row;                             // this thread's query or key
@@ -294,82 +317,71 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       if (kFirst) row_delta = __ldg(prm.delta + x);
     }
     // key rows: lse (threads 0..) and delta (threads 128..) of a step's queries
-    auto load_stat = [&](int i) -> float {
-      const bool second = tid >= 128;
-      const int c = tid & 127;
-      if (c >= kBN || (second && !kFirst)) return 0.0f;
-      int h, t0;
-      step_at<kKeys, kBN>(wk, G, i, h, t0);
-      if (t0 + c >= nq) return 0.0f;                       // masked
-      const long long x = (static_cast<long long>(wk.b) * p.Hq + h) * p.T + t0 + c;
-      return second ? __ldg(prm.delta + x) : __ldg(p.lse + x) * kLog2e;
+    const int sc = tid & 127;
+    const bool reads = kKeys && tid < (kFirst ? 256 : 128) && sc < kBN;
+    const float *stats = tid < 128 ? p.lse : prm.delta;
+    auto load_stat = [&](const Step<kKeys, kBN> &st) -> float {
+      if (!reads || st.t0 + sc >= nq) return 0.0f;         // (masked)
+      return ld_early(stats + (static_cast<long long>(wk.b) * p.Hq + st.h) * p.T + st.t0 + sc);
     };
     auto store_stat = [&](int i, float v) {
-      const int c = tid & 127;
-      if (c < kBN) stat[((i & 1) * 2 + (tid >> 7)) * kBN + c] = v;
+      if (reads) stat[((i & 1) * 2 + (tid >> 7)) * kBN + sc] = tid < 128 ? v * kLog2e : v;
     };
-    if (kKeys) store_stat(0, load_stat(0));
+    Step<kKeys, kBN> ahead(wk, G);
+    if (kKeys) store_stat(0, load_stat(ahead));
     bool ok = true;
     for (int i = 0; i < wk.n; ++i) {
-      int h, t0;
-      step_at<kKeys, kBN>(wk, G, i, h, t0);
+      const int t0 = ahead.t0;
+      ahead.next(wk);
       float next = 0.0f;
       if (kKeys) {
-        bar_sync_group(0);                                // this step's stats are there
-        if (i + 1 < wk.n) next = load_stat(i + 1);
+        bar_sync_softmax<kWarps * 32>();                   // this step's stats are there
+        if (i + 1 < wk.n) next = load_stat(ahead);
       }
-      const int sb = i % C::kNS;
-      if (!mbar_wait(&s_full[sb], (i / C::kNS) & 1, abort, kWaitNs)) {
-        give_up();
-        ok = false;
-      }
-      // (an expired wait: every thread still walks the block barriers)
-      // the columns that this row sees, as bits of 32; all of them where the whole
-      // tile is seen by every row
+      // the columns that this row sees, as bits; all of them where the whole tile is
+      // seen by every row
       bool all;
-      uint32_t bits[kHalf / 32], ds_bits[kHalf / 32];      // and those whose scores have a gradient
+      uint32_t bits = 0xFFFFFFFFu, ds_bits = 0xFFFFFFFFu;  // and those whose scores have a gradient
       if (kKeys)
         all = t0 + kBN <= nq && t0 + off >= wk.r0 + kBM - 1 &&
               (p.window == 0 || wk.r0 + kBM <= p.sinks || t0 + kBN - 1 + off < wk.r0 + p.window);
       else
         all = t0 + kBN - 1 <= min(wk.r0 + off, nk - 1) &&
               (p.window == 0 || t0 > wk.r0 + kBM - 1 + off - p.window || t0 + kBN <= p.sinks);
-#pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) {
-        bits[c] = ds_bits[c] = 0xFFFFFFFFu;
-        if (all) continue;
-        const int t1 = t0 + g * kHalf + c * 32;            // the first column's query or key
+      if (!all) {
+        const int t1 = t0 + g * kW;                        // the first column's query or key
         if (kKeys) {
           const int lo = r - off - t1;
           const int hi = (p.window > 0 && r >= p.sinks ? min(nq - t1, lo + p.window) : nq - t1) - 1;
-          bits[c] = bits_between(lo, hi);
+          bits = bits_between(lo, hi);
           // a query that sees one key: the one at position 0, or all of a window of one
-          ds_bits[c] = p.window == 1 && p.sinks == 0 ? 0u : bits[c] & ~bits_between(-off - t1, -off - t1);
+          ds_bits = p.window == 1 && p.sinks == 0 ? 0u : bits & ~bits_between(-off - t1, -off - t1);
         } else {
           const int hi = min(r + off, nk - 1) - t1;
-          bits[c] = bits_between(p.window > 0 ? r + off - p.window + 1 - t1 : 0, hi) |
-                    bits_between(0, min(hi, p.sinks - t1 - 1));
-          ds_bits[c] = attn_lone(r + off, p.window, p.sinks) ? 0u : bits[c];
+          bits = bits_between(p.window > 0 ? r + off - p.window + 1 - t1 : 0, hi) |
+                 bits_between(0, min(hi, p.sinks - t1 - 1));
+          ds_bits = attn_lone(r + off, p.window, p.sinks) ? 0u : bits;
         }
       }
-      const float *ls = stat + (i & 1) * 2 * kBN + g * kHalf;
-      const uint32_t ts = tmem + lanes + C::kTS + sb * kBN + g * kHalf;
-      float v[kHalf];
+      const int sb = i % C::kNS;
+      if (!mbar_wait(&s_full[sb], (i / C::kNS) & 1, abort, kWaitNs)) {
+        give_up();
+        ok = false;                                        // (every thread still walks the block barriers)
+      }
+      const float *ls = stat + (i & 1) * 2 * kBN + g * kW;
+      const uint32_t ts = tmem + lanes + C::kTS + sb * kBN + g * kW;
+      float v[kW];
       if (ok) {
         tc_fence_after();
-        const unsigned long long cc = pair(prm.c, prm.c);
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 32) tmem_ld32(ts + c, *reinterpret_cast<float (*)[32]>(v + c));
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 32) tmem_wait_ld32(*reinterpret_cast<float (*)[32]>(v + c));
+        ld_cols(ts, v);
         if (kFirst && !kSecond) {                          // the scores may be overwritten
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[0]);
         }
-        const unsigned long long mm = pair(-row_lse, -row_lse);
+        const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-row_lse, -row_lse);
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 4) {
+        for (int c = 0; c < kW; c += 4) {
           unsigned long long m0 = mm, m1 = mm;
           if (kKeys) {
             const float4 x = *reinterpret_cast<const float4 *>(ls + c);
@@ -378,11 +390,11 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           }
           unpair(fma2(pair(v[c], v[c + 1]), cc, m0), v[c], v[c + 1]);
           unpair(fma2(pair(v[c + 2], v[c + 3]), cc, m1), v[c + 2], v[c + 3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[c + e] = ex2(v[c + e]);
+          ex2_pair(v[c], v[c + 1]);                        // half of the pairs on the FMA pipes
+          v[c + 2] = ex2(v[c + 2]);
+          v[c + 3] = ex2(v[c + 3]);
         }
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 32) hide(*reinterpret_cast<float (*)[32]>(v + c), bits[c / 32], 0.0f);
+        hide(v, bits, 0.0f);
         // walked rows that nobody sees, zeroed before a product reads them
         bool dead = false;
         if (kKeys)
@@ -410,13 +422,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           fence_proxy_async_smem();
         }
         if (kSecond) {
-#pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = bf16x2(v[c + 2 * e], v[c + 2 * e + 1]);
-            tmem_st16u(ts + c / 2, w);
-          }
+          st_bf16(ts, v);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -429,31 +435,23 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           ok = false;
         } else {
           tc_fence_after();
-          const uint32_t td = tmem + lanes + C::kTdP + g * kHalf;
+          const uint32_t td = tmem + lanes + C::kTdP + g * kW;
           const unsigned long long dd = pair(-row_delta, -row_delta);
+          float d[kW];
+          ld_cols(td, d);
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            float d[32];
-            tmem_ld32(td + c, d);
-            tmem_wait_ld32(d);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              unsigned long long d0 = dd, d1 = dd;
-              if (kKeys) {
-                const float4 x = *reinterpret_cast<const float4 *>(ls + kBN + c + e);
-                d0 = pair(-x.x, -x.y);
-                d1 = pair(-x.z, -x.w);
-              }
-              unpair(mul2(add2(pair(d[e], d[e + 1]), d0), pair(v[c + e], v[c + e + 1])), d[e], d[e + 1]);
-              unpair(mul2(add2(pair(d[e + 2], d[e + 3]), d1), pair(v[c + e + 2], v[c + e + 3])), d[e + 2],
-                     d[e + 3]);
+          for (int e = 0; e < kW; e += 4) {
+            unsigned long long d0 = dd, d1 = dd;
+            if (kKeys) {
+              const float4 x = *reinterpret_cast<const float4 *>(ls + kBN + e);
+              d0 = pair(-x.x, -x.y);
+              d1 = pair(-x.z, -x.w);
             }
-            hide(d, ds_bits[c / 32], 0.0f);                // whatever dP holds there
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = bf16x2(d[2 * e], d[2 * e + 1]);
-            tmem_st16u(td + c / 2, w);
+            unpair(mul2(add2(pair(d[e], d[e + 1]), d0), pair(v[e], v[e + 1])), d[e], d[e + 1]);
+            unpair(mul2(add2(pair(d[e + 2], d[e + 3]), d1), pair(v[e + 2], v[e + 3])), d[e + 2], d[e + 3]);
           }
+          hide(d, ds_bits, 0.0f);                          // whatever dP holds there
+          st_bf16(td, d);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -470,7 +468,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
     if (ok) {
       tc_fence_after();
       const bool live = r < (kKeys ? nk : nq);
-      constexpr int kCols = DH / 2;                        // of this warp group
+      constexpr int kCols = DH / 4, kStep = kCols < 32 ? kCols : 32;   // of this warp group
 #pragma unroll
       for (int part = 0; part < 2; ++part) {               // first, second
         if (part == 0 ? !kFirst : !kSecond) continue;
@@ -480,22 +478,16 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         dst += kKeys ? ((static_cast<long long>(wk.b) * p.S + r) * p.Hkv + wk.kvh) * DH
                      : ((static_cast<long long>(wk.b) * p.T + r) * p.Hq + wk.h) * DH;
         float *part_dst = prm.parts + slot + static_cast<size_t>(part * kBM + row) * DH;
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 32) {
-          float o[32];
-          if (wk.n > 0) {
-            tmem_ld32(t + c, o);
-            tmem_wait_ld32(o);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-          }
+        for (int c = 0; c < kCols; c += kStep) {
+          float o[kStep];
+          ld_cols(t + c, o);
           if (!live) continue;
           if (whole_tile) {
-            store_row32(dst + g * kCols + c, o, f, prm.v8 != 0);
+            store_row(dst + g * kCols + c, o, f, prm.v8 != 0);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int e = 0; e < kStep; e += 4)
               *reinterpret_cast<float4 *>(part_dst + g * kCols + c + e) =
                   make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f);
           }
@@ -506,7 +498,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kWarps + 1) tmem_dealloc(tmem, 512);
 }
 
 template <int DH>

@@ -415,7 +415,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     // the other group's value for this row; buffers alternate from call to call
     auto exchange = [&](float x, int buffer) -> float {
       shared_max[(buffer * 2 + g) * kBM + row] = x;
-      bar_sync_group(0);
+      bar_sync_softmax<256>();
       return shared_max[(buffer * 2 + (g ^ 1)) * kBM + row];
     };
     for (unsigned r = 0, u; (u = unit_at(r)) < prm.units; ++r) {
@@ -553,7 +553,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       if constexpr (C::kG == 2) {
         l += exchange(l, j & 1);                         // the row's sum, from both groups
-        bar_sync_group(0);                               // the next unit's first tile writes there
+        bar_sync_softmax<256>();                               // the next unit's first tile writes there
       }
       if (wait(&all_done[q], nu & 1)) {
         const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
@@ -577,7 +577,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[x][e] = 0.0f;
               }
-              store_row32(dst + c + x * 32, o[x], inv, prm.v8 != 0);
+              store_row(dst + c + x * 32, o[x], inv, prm.v8 != 0);
             }
           }
         }
