@@ -109,4 +109,17 @@ __host__ __device__ __forceinline__ Steps steps_of(const QueryRange &r, int step
   return s;
 }
 
+// Steps [first, last) of one piece of a tile of n steps, pieces of even length.
+struct Piece {
+  int first, last;
+};
+
+__host__ __device__ __forceinline__ Piece piece_of(const PiecePlan &pl, int n, int piece) {
+  const int pieces = n > pl.len ? (n + pl.len - 1) / pl.len : 1;
+  const int len = (n + pieces - 1) / pieces;
+  const long long first = static_cast<long long>(piece) * len;
+  if (first >= n) return {n, n};
+  return {static_cast<int>(first), static_cast<int>(first) + (len < n - first ? len : static_cast<int>(n - first))};
+}
+
 }  // namespace rglru

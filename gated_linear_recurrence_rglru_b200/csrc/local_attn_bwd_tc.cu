@@ -21,7 +21,7 @@
 // Warps 0-15 turn scores into weights, warp group g a quarter of a tile's columns,
 // thread = row = TMEM lane; P and dS go back to TMEM as bf16 over the scores
 // they came from and are the A operand of their product. Warp 16 issues the TMA
-// copies, warp 17 the MMAs in an order that keeps the tensor core fed: the next
+// copies, warps 18 and 19 fetch lse and delta, warp 17 issues the MMAs in an order that keeps the tensor core fed: the next
 // tile's S runs while dS is formed, and P of the next tile is formed during
 // `first` and dP.
 //
@@ -38,8 +38,8 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128;
-constexpr int kWarps = 16;                             // weight warps; then copies, then MMAs
-constexpr int kThreads = (kWarps + 2) * 32;
+constexpr int kWarps = 16;                             // weight warps; then copies, MMAs, stats (2)
+constexpr int kThreads = (kWarps + 4) * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSite = 8;
@@ -59,22 +59,29 @@ struct Params {
 // kFirst: sum dS U; kSecond: sum P W.
 template <int DH, bool kFirst, bool kSecond> struct Cfg {
   static constexpr int kBN = DH == 256 ? 64 : 128;         // rows of a walked tile
+  // 256 wide: X lives in TMEM. Read from shared memory for each of a tile's 64-row
+  // products, it made S bound by shared memory's bandwidth (6 KB in 32 cycles), and
+  // its 64 KB there are a third U and a second W buffer now.
+  static constexpr bool kXT = DH == 256;
   static constexpr int kNS = kFirst ? 1 : 2;               // score buffers
-  static constexpr int kNW = DH == 256 && kFirst ? 1 : 2;  // W buffers (U has two)
+  static constexpr int kNU = kXT ? 3 : 2, kNW = kXT && !kFirst ? 3 : 2;
   static constexpr int kXBytes = kBM * DH * 2;
   static constexpr int kTile = kBN * DH * 2;
-  static constexpr int kOffY = kXBytes;
+  static constexpr int kOffY = kXT ? 0 : kXBytes;
   static constexpr int kOffU = kOffY + (kFirst ? kXBytes : 0);
-  static constexpr int kOffW = kOffU + 2 * kTile;
+  static constexpr int kOffW = kOffU + kNU * kTile;
+  static constexpr int kOffX = kXT ? kOffW : 0;            // in TMEM: on its way there
   static constexpr int kOffStat = kOffW + kNW * kTile;     // [2][lse, delta][kBN]
   static constexpr int kOffBar = kOffStat + 2 * 2 * kBN * 4;
-  static constexpr int kNumBars = 16;
+  static constexpr int kNumBars = 3 + 2 * (kNU + kNW) + 2 * 4 + 3;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16;
   static constexpr int kTSecond = kFirst ? DH : 0;         // TMEM columns
   static constexpr int kTS = kTSecond + (kSecond ? DH : 0);
   static constexpr int kTdP = kTS + kNS * kBN;
-  static_assert(kSmem <= kMaxSmem && kTdP + (kFirst ? kBN : 0) <= 512, "shared memory, TMEM");
+  static constexpr int kTX = kTdP + (kFirst ? kBN : 0);
+  static_assert(kSmem <= kMaxSmem && kTX + (kXT ? DH / 2 : 0) <= 512, "shared memory, TMEM");
+  static_assert(!kXT || kNW * kTile >= kXBytes, "X on its way to TMEM");
 };
 
 template <int DH> constexpr int smem_bytes() {
@@ -83,13 +90,6 @@ template <int DH> constexpr int smem_bytes() {
                                                                       : Cfg<256, false, true>::kSmem;
   else
     return Cfg<DH, true, true>::kSmem;
-}
-
-// A load that stays where it is written: issued now, used a step later.
-__device__ __forceinline__ float ld_early(const float *p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
 }
 
 // Where a block stands: its rows, and the walk over the other side.
@@ -140,24 +140,33 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int G = p.Hq / p.Hkv, off = p.S - p.T;
   uint64_t *x_full = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
-  uint64_t *u_full = x_full + 1, *u_empty = u_full + 2;
-  uint64_t *w_full = u_empty + 2, *w_empty = w_full + 2;
-  uint64_t *s_full = w_empty + 2;                     // [kNS]
-  uint64_t *p_full = s_full + 2;                      // [kNS] P is in TMEM (kSecond) or S was read
-  uint64_t *dp_full = p_full + 2, *ds_full = dp_full + 1, *done = ds_full + 1;
-  static_assert(C::kNumBars >= 16, "barriers");
+  uint64_t *y_full = x_full + 1, *x_done = y_full + 1;    // x_done: X is in TMEM
+  uint64_t *u_full = x_done + 1, *u_empty = u_full + C::kNU;
+  uint64_t *w_full = u_empty + C::kNU, *w_empty = w_full + C::kNW;
+  uint64_t *s_full = w_empty + C::kNW;                    // [kNS]
+  uint64_t *p_full = s_full + 2;                          // [kNS] P is in TMEM (kSecond) or S was read
+  uint64_t *stat_full = p_full + 2, *stat_empty = stat_full + 2;   // [2] key rows
+  uint64_t *dp_full = stat_empty + 2, *ds_full = dp_full + 1, *done = ds_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + C::kOffMisc + 4);
   float *stat = reinterpret_cast<float *>(sm + C::kOffStat);
   if (tid == 0) {
     mbar_init(x_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    mbar_init(y_full, 1);
+    mbar_init(x_done, kWarps);
+    for (int s = 0; s < C::kNU; ++s) {
       mbar_init(&u_full[s], 1);
       mbar_init(&u_empty[s], 1);
+    }
+    for (int s = 0; s < C::kNW; ++s) {
       mbar_init(&w_full[s], 1);
       mbar_init(&w_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], kWarps);
+      mbar_init(&stat_full[s], 2);
+      mbar_init(&stat_empty[s], kWarps);
     }
     mbar_init(dp_full, 1);
     mbar_init(ds_full, kWarps);
@@ -185,16 +194,19 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
     // ============================ TMA producer ============================
     if (lane == 0) {
       const int xh = kKeys ? wk.kvh : wk.h;
-      mbar_arrive_expect_tx(x_full, C::kXBytes * (kFirst ? 2 : 1));
-      for (int c = 0; c < DH / 64; ++c) {
-        tma_load_4d(sm + c * (kBM * 128), mx, x_full, c * 64, wk.r0, xh, wk.b);
-        if (kFirst) tma_load_4d(sm + C::kOffY + c * (kBM * 128), my, x_full, c * 64, wk.r0, xh, wk.b);
+      mbar_arrive_expect_tx(x_full, C::kXBytes);
+      for (int c = 0; c < DH / 64; ++c)
+        tma_load_4d(sm + C::kOffX + c * (kBM * 128), mx, x_full, c * 64, wk.r0, xh, wk.b);
+      if (kFirst) {
+        mbar_arrive_expect_tx(y_full, C::kXBytes);
+        for (int c = 0; c < DH / 64; ++c)
+          tma_load_4d(sm + C::kOffY + c * (kBM * 128), my, y_full, c * 64, wk.r0, xh, wk.b);
       }
       int w_issued = 0, u_issued = 0;
       for (Step<kKeys, kBN> st(wk, G); st.i < wk.n; st.next(wk)) {
         const int i = st.i, h = st.h, t0 = st.t0;
-        const int u = i & 1, w = i % C::kNW;
-        if (!mbar_wait(&u_empty[u], ((i >> 1) & 1) ^ 1, abort, kWaitNs)) {
+        const int u = i % C::kNU, w = i % C::kNW;
+        if (!mbar_wait(&u_empty[u], ((i / C::kNU) & 1) ^ 1, abort, kWaitNs)) {
           give_up();
           break;
         }
@@ -202,7 +214,9 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         for (int c = 0; c < DH / 64; ++c)
           tma_load_4d(sm + C::kOffU + u * C::kTile + c * (kBN * 128), mu, &u_full[u], c * 64, t0, h, wk.b);
         u_issued = i + 1;
-        if (!mbar_wait(&w_empty[w], ((i / C::kNW) & 1) ^ 1, abort, kWaitNs)) {
+        // the W buffers hold X on its way to TMEM at first
+        if ((C::kXT && i == 0 && !mbar_wait(x_done, 0, abort, kWaitNs)) ||
+            !mbar_wait(&w_empty[w], ((i / C::kNW) & 1) ^ 1, abort, kWaitNs)) {
           give_up();
           break;
         }
@@ -213,10 +227,36 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       }
       if (*abort) {
         mbar_wait_drain(x_full, 0, kDrainNs);
-        for (int j = u_issued - 1; j >= 0 && j >= u_issued - 2; --j)
-          mbar_wait_drain(&u_full[j & 1], (j >> 1) & 1, kDrainNs);
+        if (kFirst) mbar_wait_drain(y_full, 0, kDrainNs);
+        for (int j = u_issued - 1; j >= 0 && j >= u_issued - C::kNU; --j)
+          mbar_wait_drain(&u_full[j % C::kNU], (j / C::kNU) & 1, kDrainNs);
         for (int j = w_issued - 1; j >= 0 && j >= w_issued - C::kNW; --j)
           mbar_wait_drain(&w_full[j % C::kNW], (j / C::kNW) & 1, kDrainNs);
+      }
+    }
+  } else if (warp >= kWarps + 2) {
+    // ===================== lse and delta of key rows' queries =====================
+    if (kKeys) {
+      const int second = warp - (kWarps + 2);             // the lse's warp, the delta's
+      const float *src = second ? prm.delta : p.lse;
+      const float f = second ? 1.0f : kLog2e;
+      for (Step<kKeys, kBN> st(wk, G); st.i < wk.n; st.next(wk)) {
+        float v[kBN / 32] = {};
+        if (!second || kFirst) {
+          const float *row = src + (static_cast<long long>(wk.b) * p.Hq + st.h) * p.T;
+#pragma unroll
+          for (int x = 0; x < kBN / 32; ++x)
+            if (st.t0 + x * 32 + lane < wk.len.nq) v[x] = __ldg(row + st.t0 + x * 32 + lane) * f;
+        }
+        const int s = st.i & 1;
+        if (!mbar_wait(&stat_empty[s], ((st.i >> 1) & 1) ^ 1, abort, kWaitNs)) {
+          give_up();
+          break;
+        }
+#pragma unroll
+        for (int x = 0; x < kBN / 32; ++x) stat[(s * 2 + second) * kBN + x * 32 + lane] = v[x];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stat_full[s]);
       }
     }
   } else if (warp == kWarps + 1) {
@@ -242,7 +282,15 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         mma_ss(d, ad + (((k & 3) * 32 + (k >> 2) * (kBM * 128)) >> 4),
                bd + (((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4), id_s, k > 0 ? 1u : 0u);
     };
-    // (one lane) weights in TMEM (each half of the columns at the start of its
+    // (one lane) the same with the rows in TMEM
+    auto scores_t = [&](uint32_t d, uint32_t tile) {
+      const uint32_t bd = desc_lo(base + tile, 16);
+#pragma unroll
+      for (int k = 0; k < DH / 16; ++k)
+        mma_ts(d, tmem + C::kTX + k * 8, bd + (((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4), id_s,
+               k > 0 ? 1u : 0u);
+    };
+    // (one lane) weights in TMEM (each group's columns at the start of its
     // scores) times tile (MN-major): D += A T
     auto product = [&](uint32_t d, uint32_t a, uint32_t tile, bool add) {
       const uint32_t bd = desc_lo(base + tile, kBN * 128);
@@ -251,14 +299,17 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         mma_ts(d, a + (k / (kW / 16)) * kW + (k % (kW / 16)) * 8, bd + ((k * 16 * 128) >> 4),
                id_o, k > 0 ? 1u : add);
     };
-    auto u_at = [&](int i) { return static_cast<uint32_t>(C::kOffU + (i & 1) * C::kTile); };
+    auto u_at = [&](int i) { return static_cast<uint32_t>(C::kOffU + (i % C::kNU) * C::kTile); };
     auto w_at = [&](int i) { return static_cast<uint32_t>(C::kOffW + (i % C::kNW) * C::kTile); };
     auto issue_s = [&](int i) {
-      if (!wait(&u_full[i & 1], (i >> 1) & 1)) return;
+      if (!wait(&u_full[i % C::kNU], (i / C::kNU) & 1)) return;
       if (elect_one()) {
-        scores(tmem + C::kTS + (i % C::kNS) * kBN, 0, u_at(i));
+        if (C::kXT)
+          scores_t(tmem + C::kTS + (i % C::kNS) * kBN, u_at(i));
+        else
+          scores(tmem + C::kTS + (i % C::kNS) * kBN, C::kOffX, u_at(i));
         mma_commit(&s_full[i % C::kNS]);
-        if (!kFirst) mma_commit(&u_empty[i & 1]);
+        if (!kFirst) mma_commit(&u_empty[i % C::kNU]);
       }
       __syncwarp();
     };
@@ -279,9 +330,9 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       }
       __syncwarp();
     };
-    wait(x_full, 0);
+    wait(C::kXT ? x_done : x_full, 0);
     if (ok) issue_s(0);
-    if (kFirst && ok) issue_dp(0);
+    if (kFirst && wait(y_full, 0)) issue_dp(0);
     for (int i = 0; i < wk.n && ok; ++i) {
       if (!kFirst) {
         if (i + 1 < wk.n) issue_s(i + 1);
@@ -295,7 +346,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       if (wait(ds_full, i & 1)) {
         if (elect_one()) {
           product(tmem, tmem + C::kTdP, u_at(i), i > 0);
-          mma_commit(&u_empty[i & 1]);
+          mma_commit(&u_empty[i % C::kNU]);
         }
         __syncwarp();
         if (i + 1 < wk.n) issue_dp(i + 1);
@@ -316,28 +367,38 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
       row_lse = __ldg(p.lse + x) * kLog2e;
       if (kFirst) row_delta = __ldg(prm.delta + x);
     }
-    // key rows: lse (threads 0..) and delta (threads 128..) of a step's queries
-    const int sc = tid & 127;
-    const bool reads = kKeys && tid < (kFirst ? 256 : 128) && sc < kBN;
-    const float *stats = tid < 128 ? p.lse : prm.delta;
-    auto load_stat = [&](const Step<kKeys, kBN> &st) -> float {
-      if (!reads || st.t0 + sc >= nq) return 0.0f;         // (masked)
-      return ld_early(stats + (static_cast<long long>(wk.b) * p.Hq + st.h) * p.T + st.t0 + sc);
-    };
-    auto store_stat = [&](int i, float v) {
-      if (reads) stat[((i & 1) * 2 + (tid >> 7)) * kBN + sc] = tid < 128 ? v * kLog2e : v;
-    };
-    Step<kKeys, kBN> ahead(wk, G);
-    if (kKeys) store_stat(0, load_stat(ahead));
     bool ok = true;
-    for (int i = 0; i < wk.n; ++i) {
-      const int t0 = ahead.t0;
-      ahead.next(wk);
-      float next = 0.0f;
-      if (kKeys) {
-        bar_sync_softmax<kWarps * 32>();                   // this step's stats are there
-        if (i + 1 < wk.n) next = load_stat(ahead);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
+        give_up();
+        ok = false;
       }
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    if constexpr (C::kXT) {                                // X to TMEM: 64 columns of a row a thread
+      if (wait(x_full, 0)) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(sm + C::kOffX + g * (kBM * 128) + row * 128 +
+                                                           ((c ^ (row & 7)) << 4));
+          w[4 * c] = x.x;
+          w[4 * c + 1] = x.y;
+          w[4 * c + 2] = x.z;
+          w[4 * c + 3] = x.w;
+        }
+        tmem_st32u(tmem + lanes + C::kTX + g * 32, w);
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_done);
+      }
+    }
+    Step<kKeys, kBN> st(wk, G);
+    for (int i = 0; i < wk.n && ok; ++i, st.next(wk)) {
+      const int t0 = st.t0;
       // the columns that this row sees, as bits; all of them where the whole tile is
       // seen by every row
       bool all;
@@ -364,15 +425,12 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         }
       }
       const int sb = i % C::kNS;
-      if (!mbar_wait(&s_full[sb], (i / C::kNS) & 1, abort, kWaitNs)) {
-        give_up();
-        ok = false;                                        // (every thread still walks the block barriers)
-      }
       const float *ls = stat + (i & 1) * 2 * kBN + g * kW;
       const uint32_t ts = tmem + lanes + C::kTS + sb * kBN + g * kW;
       float v[kW];
-      if (ok) {
-        tc_fence_after();
+      if (kKeys && !wait(&stat_full[i & 1], (i >> 1) & 1)) break;
+      if (!wait(&s_full[sb], (i / C::kNS) & 1)) break;
+      {
         ld_cols(ts, v);
         if (kFirst && !kSecond) {                          // the scores may be overwritten
           tc_fence_before();
@@ -390,7 +448,12 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           }
           unpair(fma2(pair(v[c], v[c + 1]), cc, m0), v[c], v[c + 1]);
           unpair(fma2(pair(v[c + 2], v[c + 3]), cc, m1), v[c + 2], v[c + 3]);
-          ex2_pair(v[c], v[c + 1]);                        // half of the pairs on the FMA pipes
+          if (c % 8 == 0) {                                // a quarter of them on the FMA pipes
+            ex2_pair(v[c], v[c + 1]);
+          } else {
+            v[c] = ex2(v[c]);
+            v[c + 1] = ex2(v[c + 1]);
+          }
           v[c + 2] = ex2(v[c + 2]);
           v[c + 3] = ex2(v[c + 3]);
         }
@@ -402,21 +465,15 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         else
           dead = dead_keys(p, nk).any(t0, kBN);
         if (dead) {
-          if (kFirst && kSecond && !mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
-            give_up();
-            ok = false;
-          }
-          if (!kFirst && !mbar_wait(&w_full[i % C::kNW], (i / C::kNW) & 1, abort, kWaitNs)) {
-            give_up();
-            ok = false;
-          }
+          if (kFirst && kSecond && !wait(dp_full, i & 1)) break;
+          if (!kFirst && !wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) break;
           const bool mine = tid < kBN && (kKeys ? t0 + tid >= nq : dead_keys(p, nk).in(t0 + tid));
-          if (ok && mine)
+          if (mine)
             for (int c = 0; c < DH / 64; ++c)
               for (int e = 0; e < 8; ++e) {
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 const int o = c * (kBN * 128) + tid * 128 + e * 16;
-                if (kFirst) *reinterpret_cast<uint4 *>(sm + C::kOffU + (i & 1) * C::kTile + o) = z;
+                if (kFirst) *reinterpret_cast<uint4 *>(sm + C::kOffU + (i % C::kNU) * C::kTile + o) = z;
                 if (kSecond) *reinterpret_cast<uint4 *>(sm + C::kOffW + (i % C::kNW) * C::kTile + o) = z;
               }
           fence_proxy_async_smem();
@@ -429,12 +486,9 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           if (lane == 0) mbar_arrive(&p_full[sb]);
         }
       }
-      if (kFirst && ok) {
-        if (!mbar_wait(dp_full, i & 1, abort, kWaitNs)) {
-          give_up();
-          ok = false;
-        } else {
-          tc_fence_after();
+      if (kFirst) {
+        if (!wait(dp_full, i & 1)) break;
+        {
           const uint32_t td = tmem + lanes + C::kTdP + g * kW;
           const unsigned long long dd = pair(-row_delta, -row_delta);
           float d[kW];
@@ -458,15 +512,12 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           if (lane == 0) mbar_arrive(ds_full);
         }
       }
-      if (kKeys && i + 1 < wk.n) store_stat(i + 1, next);
-      if (!kKeys && !ok) break;
+      if (kKeys) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stat_empty[i & 1]);
+      }
     }
-    if (ok && !mbar_wait(done, 0, abort, kWaitNs)) {
-      give_up();
-      ok = false;
-    }
-    if (ok) {
-      tc_fence_after();
+    if (wait(done, 0)) {
       const bool live = r < (kKeys ? nk : nq);
       constexpr int kCols = DH / 4, kStep = kCols < 32 ? kCols : 32;   // of this warp group
 #pragma unroll
@@ -530,10 +581,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap q_rows, const __grid_cons
     w.r0 = at.tile * kBM;
     if (w.r0 >= w.len.nk) return;
     w.st = steps_of(query_range(w.r0, kBM, w.len.nq, w.len.nk, off, p.window, p.sinks), kBN, G);
-    w.first = at.piece * prm.pl.len;
-    const int last = min(w.first + prm.pl.len, w.st.n);
-    if (w.first >= last && at.piece > 0) return;
-    w.n = max(last - w.first, 0);
+    const Piece pc = piece_of(prm.pl, w.st.n, at.piece);
+    if (pc.first >= pc.last && at.piece > 0) return;
+    w.first = pc.first;
+    w.n = pc.last - pc.first;
     const bool whole = w.st.n <= prm.pl.len;
     const size_t slot =
         (static_cast<size_t>(bk) * prm.pl.slots + first_slot(prm.pl, at.tile) + at.piece) * 2 * kBM * DH;
@@ -581,8 +632,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap q_rows, const __grid_cons
   walk<DH, false, true, false>(prm, &q_rows, &do_rows, &k_tile, &v_tile, w, true, 0, sm);
 }
 
+// A call's steps are its key-row steps (twice for 256-wide heads) and about as many
+// query-row steps, over 148 SMs. A tile of keys is cut only where one piece would be
+// longer than 1.15 times an SM's share of them: a cut costs partial sums that are written and
+// read again (4 rows of 2048, 10 query heads on one 256-wide key head: 257 us
+// without cuts, 283 us with pieces of half, 318 us of a fifth of a tile).
 PiecePlan plan_of(const AttnArgs &p) {
-  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, kBM, p.dh == 256 ? 64 : 128, 2 * 148);
+  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, kBM, p.dh == 256 ? 64 : 128,
+                   p.dh == 256 ? 43 : 64);
 }
 
 template <int DH>

@@ -343,7 +343,8 @@ attn_dkv_generic_kernel(const AttnArgs p, const float *delta, const PiecePlan pl
   const RowLens n = row_lens(p, b);
   if (k0 >= n.nk) return;
   const Steps st = steps_of(query_range(k0, BT, n.nq, n.nk, off, p.window, p.sinks), BT, G);
-  const int first = at.piece * pl.len, last = min(first + pl.len, st.n);
+  const Piece pc = piece_of(pl, st.n, at.piece);
+  const int first = pc.first, last = pc.last;
   if (first >= last && at.piece > 0) return;
   fill<T, BT, NC>(ks, head_of<T>(p.k, b, kvh), p.k.st, k0, n.nk, p.dh);
   fill<T, BT, NC>(vs, head_of<T>(p.v, b, kvh), p.v.st, k0, n.nk, p.dh);
@@ -450,7 +451,9 @@ attn_join_kernel(const AttnArgs p, const PiecePlan pl, const float *__restrict__
   const Steps st = steps_of(query_range(k0, pl.tile, n.nq, n.nk, off, p.window, p.sinks), pl.step,
                             p.Hq / p.Hkv);
   if (k0 >= n.nk || st.n <= pl.len) return;         // stored by its only piece
-  const int np = (st.n + pl.len - 1) / pl.len;
+  // the pieces that are not empty (rounding the even length up can leave the last so)
+  const int asked = (st.n + pl.len - 1) / pl.len, each = (st.n + asked - 1) / asked;
+  const int np = (st.n + each - 1) / each;
   const size_t one = static_cast<size_t>(2) * pl.tile * p.dh;
   const float *src = parts + (static_cast<size_t>(blockIdx.z) * pl.slots + first_slot(pl, tile)) * one;
   const int per_row = p.dh / 4;
@@ -506,7 +509,7 @@ int generic_tile(int dh) { return dh <= 128 ? 64 : 32; }
 
 PiecePlan generic_plan_of(const AttnArgs &p) {
   const int bt = generic_tile(p.dh);
-  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 2 * 148);
+  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 148);
 }
 
 template <typename T> cudaError_t bwd_typed(const AttnArgs &p, void *ws, cudaStream_t st) {
