@@ -31,7 +31,8 @@ __all__ += _ATTENTION
 def __getattr__(name):
     if name in _ATTENTION:
         from . import attention
-        return getattr(attention, name)
+        globals().update({n: getattr(attention, n) for n in _ATTENTION})
+        return globals()[name]
     if name in __all__:
         from . import _abi
         return getattr(_abi, name)
