@@ -7,9 +7,9 @@
 //   backward   P = exp(S - lse), dP = dO V^T, dS = P (dP - delta),
 //              delta = rowsum(dO * O); dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO
 //
-// Bound by the CUDA cores' fp32 rate. Tiles of BT queries by BT keys (64, or 32
-// for heads over 128 wide, whose four operand tiles fill shared memory) in
-// float in shared memory; 16 x 16 threads, each BT/16 rows by BT/16 columns of
+// Bound by the CUDA cores' fp32 rate. Tiles of BT queries by BT keys (64, or, in
+// the backward of heads over 128 wide, whose four operand tiles fill shared memory,
+// 48) in float in shared memory; 16 x 16 threads, each BT/16 rows by BT/16 columns of
 // S and BT/16 rows by dh/16 columns of a product, from 16-byte shared loads.
 // Rows of shared memory are padded by 16 bytes, so the 8 rows that a quarter
 // warp reads fall into different banks. Tiles outside the mask are skipped.
@@ -44,6 +44,28 @@ __device__ __forceinline__ void fill(float *dst, const T *src, long long st, int
     }
     *reinterpret_cast<float4 *>(dst + r * kPitch + c) = v;
   }
+}
+
+// The same ahead of use: fp32 rows by cp.async, in flight until fill_wait.
+template <typename T, int BT, int NC>
+__device__ __forceinline__ void fill_ahead(float *dst, const T *src, long long st, int r0, int n, int dh) {
+  if constexpr (sizeof(T) == 4) {
+    constexpr int W = NC * 64, kPitch = W + 4, kV = W / 4;
+    for (int i = threadIdx.x; i < BT * kV; i += kThreads) {
+      const int r = i / kV, c = (i % kV) * 4;
+      const bool in = r0 + r < n && c < dh;
+      const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * kPitch + c));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                   "l"(in ? src + (r0 + r) * st + c : src), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    fill<T, BT, NC>(dst, src, st, r0, n, dh);
+  }
+}
+__device__ __forceinline__ void fill_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void fill_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // acc[i][j] = sum_d a[ty + 16 i][d] b[tx + 16 j][d]
@@ -141,7 +163,7 @@ __device__ __forceinline__ float row_sum16(float v) {
 }
 
 template <int BT, int NC> constexpr int fwd_smem() {
-  return (3 * BT * (NC * 64 + 4) + BT * (BT + 4)) * 4;
+  return (5 * BT * (NC * 64 + 4) + BT * (BT + 4)) * 4;
 }
 template <int BT, int NC> constexpr int bwd_smem() {
   return (4 * BT * (NC * 64 + 4) + 2 * BT * (BT + 4) + 2 * BT) * 4;
@@ -151,10 +173,11 @@ template <typename T, int BT, int NC>
 __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnArgs p) {
   extern __shared__ __align__(16) float smf[];
   constexpr int kPitch = NC * 64 + 4, N = BT / 16, kWp = BT + 4;
-  float *qs = smf, *ks = qs + BT * kPitch, *vs = ks + BT * kPitch, *ps = vs + BT * kPitch;
+  float *qs = smf, *kvs = qs + BT * kPitch, *ps = kvs + 4 * BT * kPitch;   // K and V: two buffers
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int h = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
-  const int q0 = blockIdx.y * BT, off = p.S - p.T;
+  // the last queries first: they see the most keys
+  const int q0 = (gridDim.y - 1 - blockIdx.y) * BT, off = p.S - p.T;
   const RowLens n = row_lens(p, b);
   if (q0 >= n.nq) return;
   const int kvh = h / (p.Hq / p.Hkv);
@@ -173,11 +196,20 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
   }
   // positions of the tile's queries bound which keys any of them sees
   const int seen_lo = p.window > 0 ? q0 + off - p.window + 1 : 0, seen_hi = qe + off;
+  auto ahead = [&](int x) {
+    if (x < kt.n) {
+      float *d = kvs + (x & 1) * 2 * BT * kPitch;
+      fill_ahead<T, BT, NC>(d, kp, p.k.st, kt.tile(x) * BT, n.nk, p.dh);
+      fill_ahead<T, BT, NC>(d + BT * kPitch, vp, p.v.st, kt.tile(x) * BT, n.nk, p.dh);
+    }
+    fill_commit();
+  };
+  ahead(0);
   for (int x = 0; x < kt.n; ++x) {
     const int k0 = kt.tile(x) * BT;
-    __syncthreads();
-    fill<T, BT, NC>(ks, kp, p.k.st, k0, n.nk, p.dh);
-    fill<T, BT, NC>(vs, vp, p.v.st, k0, n.nk, p.dh);
+    float *ks = kvs + (x & 1) * 2 * BT * kPitch, *vs = ks + BT * kPitch;
+    ahead(x + 1);
+    fill_wait<1>();
     __syncthreads();
     // value rows that no query here sees count as zeros, whatever they hold
     for (int i = threadIdx.x; i < BT * NC * 16; i += kThreads) {
@@ -220,7 +252,9 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
     }
     __syncthreads();
     add_product<BT, NC, false>(o, ps, vs, tx, ty);
+    __syncthreads();                               // the buffer may be filled again
   }
+  fill_wait<0>();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int t = q0 + ty + 16 * i;
@@ -272,7 +306,7 @@ attn_dq_generic_kernel(const AttnArgs p, const float *delta) {
   float *dss = vs + BT * kPitch, *lses = dss + 2 * BT * kWp, *deltas = lses + BT;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int h = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
-  const int q0 = blockIdx.y * BT, off = p.S - p.T;
+  const int q0 = (gridDim.y - 1 - blockIdx.y) * BT, off = p.S - p.T;
   const RowLens n = row_lens(p, b);
   if (q0 >= n.nq) return;
   const int kvh = h / (p.Hq / p.Hkv);
@@ -505,10 +539,10 @@ cudaError_t run_bwd(const AttnArgs &p, const float *delta, const PiecePlan &pl, 
   return cudaGetLastError();
 }
 
-int generic_tile(int dh) { return dh <= 128 ? 64 : 32; }
+int bwd_tile(int dh) { return dh <= 128 ? 64 : 48; }
 
 PiecePlan generic_plan_of(const AttnArgs &p) {
-  const int bt = generic_tile(p.dh);
+  const int bt = bwd_tile(p.dh);
   return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 148);
 }
 
@@ -521,8 +555,8 @@ template <typename T> cudaError_t bwd_typed(const AttnArgs &p, void *ws, cudaStr
   switch (ceil_div(p.dh, 64)) {
     case 1: e = run_bwd<T, 64, 1>(p, delta, pl, parts, st); break;
     case 2: e = run_bwd<T, 64, 2>(p, delta, pl, parts, st); break;
-    case 3: e = run_bwd<T, 32, 3>(p, delta, pl, parts, st); break;
-    default: e = run_bwd<T, 32, 4>(p, delta, pl, parts, st); break;
+    case 3: e = run_bwd<T, 48, 3>(p, delta, pl, parts, st); break;
+    default: e = run_bwd<T, 48, 4>(p, delta, pl, parts, st); break;
   }
   if (e != cudaSuccess) return e;
   return launch_attn_join(p, sizeof(T) == 4 ? RGLRU_IO_F32 : RGLRU_IO_BF16, pl, parts, st);
@@ -532,7 +566,7 @@ template <typename T> cudaError_t fwd_typed(const AttnArgs &p, cudaStream_t st) 
   switch (ceil_div(p.dh, 64)) {
     case 1: return run_fwd<T, 64, 1>(p, st);
     case 2: return run_fwd<T, 64, 2>(p, st);
-    case 3: return run_fwd<T, 32, 3>(p, st);
+    case 3: return run_fwd<T, 48, 3>(p, st);
     default: return run_fwd<T, 32, 4>(p, st);
   }
 }
