@@ -185,13 +185,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 2^a, 2^b for a, b <= 127 on the FMA pipes: 2^x = 2^n 2^f with n the nearest whole
 // number (read off the low bits of x + 1.5 * 2^23) and f in [-1/2, 1/2], 2^f by the
 // polynomial of degree 4 of least relative error there (2.6e-6, by Remez exchange),
-// n added to the exponent. Below -126 the result is 2^-126 to a factor of sqrt 2.
+// n added to the exponent. Below -126 the result is 2^-126 to a factor of sqrt 2; for
+// NaN it is NaN or over 3e38.
 __device__ __forceinline__ void ex2_pair(float &a, float &b) {
   constexpr float kMagic = 12582912.0f;
-  const unsigned long long x = pair(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+  const unsigned long long x = pair(max_nan(a, -126.0f), max_nan(b, -126.0f));
   const unsigned long long z = add2(x, pair(kMagic, kMagic));
   const unsigned long long n = add2(z, pair(-kMagic, -kMagic));
   const unsigned long long f = fma2(n, pair(-1.0f, -1.0f), x);

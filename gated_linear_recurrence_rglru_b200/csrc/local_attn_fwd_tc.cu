@@ -512,7 +512,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               tmem_ld32(ts + c, w);
               tmem_wait_ld32(w);
               hide(w, bits, -INFINITY);
-              weights32<C::kPoly>(w, cc, mm, sum, packed);
+              weights32<0>(w, cc, mm, sum, packed);      // hidden scores give 0 exactly
             }
             tmem_st16u(ts + c / 2, packed);
           }
@@ -556,7 +556,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         bar_sync_softmax<256>();                               // the next unit's first tile writes there
       }
       if (wait(&all_done[q], nu & 1)) {
-        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        // (a row that sees a key has a weight of 1 at least; NaN scores leave l NaN)
+        const bool none = l == 0.0f;
+        const float inv = none ? 0.0f : 1.0f / l;
         __nv_bfloat16 *dst = out + out_row * DH + g * kOut;
 #pragma unroll 1
         for (int c = 0; c < kOut; c += 64) {
@@ -573,7 +575,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           if (live) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (m == -INFINITY) {
+              if (none) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[x][e] = 0.0f;
               }
@@ -582,7 +584,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
         }
         if (live && g == 0 && p.lse != nullptr)
-          p.lse[lse_row] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+          p.lse[lse_row] = none ? -INFINITY : m * kLn2 + logf(l);
       }
       ++nu;
     }

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float w = mn == -INFINITY ? 0.0f : expf(s[i][j] - mn);
+        const float w = s[i][j] == -INFINITY ? 0.0f : expf(s[i][j] - mn);   // (NaN stays NaN)
         sum += w;
         ps[(ty + 16 * i) * kWp + tx + 16 * j] = w;
       }
@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
   for (int i = 0; i < N; ++i) {
     const int t = q0 + ty + 16 * i;
     if (t >= n.nq) continue;
-    const float inv = l[i] > 0.0f ? 1.0f / l[i] : (m[i] == -INFINITY ? 0.0f : 1.0f / l[i]);
+    const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
     T *dst = static_cast<T *>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
       if (tx * 4 + c * 64 < p.dh) store4<T>(dst + tx * 4 + c * 64, o[i][c], inv);
     if (p.lse != nullptr && tx == 0)
       p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] =
-          m[i] == -INFINITY ? -INFINITY : m[i] + logf(l[i]);
+          l[i] == 0.0f ? -INFINITY : m[i] + logf(l[i]);
   }
 }
 

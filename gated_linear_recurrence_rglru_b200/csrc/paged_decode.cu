@@ -328,7 +328,7 @@ paged_decode_kernel(const DecodeArgs p, const Parts parts, int slices) {
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
       const float2 ml = ml_s[w * 16 + row];
-      const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mm);
+      const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - mm);   // (NaN scores leave NaN sums)
       const float4 v = *reinterpret_cast<const float4 *>(os + (w * 16 + row) * DH + d);
       ll = fmaf(f, ml.y, ll);
       acc.x = fmaf(f, v.x, acc.x);
@@ -337,7 +337,7 @@ paged_decode_kernel(const DecodeArgs p, const Parts parts, int slices) {
       acc.w = fmaf(f, v.w, acc.w);
     }
     if (parts.chunks == 1) {
-      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + (hrow + row) * DH + d) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     } else {
@@ -474,7 +474,7 @@ paged_decode_generic_kernel(const DecodeArgs p, const Parts parts, int slices) {
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
       const float mn = fmaxf(m, mx);
-      const float w = mn == -INFINITY ? 0.0f : exp2f(s - mn);
+      const float w = s == -INFINITY ? 0.0f : exp2f(s - mn);
       const float f = m == -INFINITY ? 0.0f : exp2f(m - mn);
       float sum = w;
 #pragma unroll
@@ -517,7 +517,7 @@ paged_decode_generic_kernel(const DecodeArgs p, const Parts parts, int slices) {
     for (int x = 0; x < groups; ++x) s += red[x * kGenHeads * dh + i];
     const float2 ml = mls[h];
     if (parts.chunks == 1) {
-      static_cast<T *>(p.out)[hrow * dh + i] = from_f32<T>(ml.y > 0.0f ? s / ml.y : 0.0f);
+      static_cast<T *>(p.out)[hrow * dh + i] = from_f32<T>(ml.y == 0.0f ? 0.0f : s / ml.y);
     } else {
       const long long part = (hrow + h) * parts.chunks + un.c;
       parts.o[part * dh + i % dh] = s;
@@ -559,7 +559,7 @@ decode_join_kernel(const DecodeArgs p, const Parts parts) {
     for (int c = gr; c < n; c += groups) {
       const float2 ml = parts.ml[row + c];
       const float4 v = *reinterpret_cast<const float4 *>(parts.o + (row + c) * dh + col * 4);
-      const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mm);
+      const float f = ml.y == 0.0f ? 0.0f : exp2f(ml.x - mm);
       l = fmaf(f, ml.y, l);
       a.x = fmaf(f, v.x, a.x);
       a.y = fmaf(f, v.y, a.y);
@@ -579,7 +579,7 @@ decode_join_kernel(const DecodeArgs p, const Parts parts) {
     a.w += v.w;
     l += red_l[x * cols + tid];
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   T *o = static_cast<T *>(p.out) + static_cast<long long>(blockIdx.x) * dh + tid * 4;
   o[0] = from_f32<T>(a.x * inv);
   o[1] = from_f32<T>(a.y * inv);

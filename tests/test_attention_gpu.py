@@ -281,6 +281,26 @@ def test_local_attn_bwd(cuda_device, case):
         assert all(torch.equal(got[n][b, :m], again[n][b, :m]) for n in grads for b, m in enumerate(lens))
 
 
+@pytest.mark.parametrize("io,dh,T,G", [("bf16", 64, 300, 2), ("bf16", 128, 40, 1), ("bf16", 256, 200, 2),
+                                       ("f32", 64, 90, 2), ("f32", 256, 40, 1)])
+def test_nan_reaches_who_sees_it_alone(cuda_device, io, dh, T, G):
+    """A NaN in a query is that query's output; a NaN in a key that of the queries that see it."""
+    gen = torch.Generator().manual_seed(61)
+    q, k, v = (randn(gen, (1, T, h, dh), io).to(cuda_device) for h in (2, 2 // G, 2 // G))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v)
+    q2, k2 = q.clone(), k.clone()
+    q2[0, 5, 1, 3] = float("nan")
+    got, glse = rg.rglru_local_attn_fwd(q2, k, v)
+    assert torch.isnan(got[0, 5, 1]).all() and torch.isnan(glse[0, 1, 5])
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[0, 5, 1] = False
+    assert torch.equal(got[keep], out[keep]) and int(torch.isnan(glse).sum()) == 1
+    k2[0, 20, 0, 0] = float("nan")
+    got, glse = rg.rglru_local_attn_fwd(q, k2, v)
+    assert torch.equal(got[:, :20], out[:, :20]) and torch.equal(glse[..., :20], lse[..., :20])
+    assert torch.isnan(got[:, 20:, 0]).all() and torch.isnan(glse[:, 0, 20:]).all()
+
+
 # ---------------------------------------------------------------- one token over a cache
 
 DECODE_CASES = [  # io, Hq, Hkv, dh, page, lens, window, sinks, max_pages
@@ -325,6 +345,20 @@ def test_paged_attn_decode(cuda_device, case):
     w = 2 * score_error(host[0], host[1], dh, scale) + (max(lens) + 16) * 2 * U
     close(got, ref, w * size + (UB * (size + np.abs(ref)) if io == "bf16" else 0), "out")
     assert torch.equal(rg.rglru_paged_attn_decode(*d, window=window, sinks=sinks), got)
+
+
+@pytest.mark.parametrize("io,dh,lens", [("bf16", 128, [60, 3000]), ("bf16", 256, [60, 50]), ("f32", 64, [60, 9000])])
+def test_paged_attn_decode_nan(cuda_device, io, dh, lens):
+    case = (io, 4, 2, dh, 16, lens, 0, 0, max(lens) // 16 + 1)
+    d = [x.to(cuda_device) for x in decode_inputs(case, 23)]
+    out = rg.rglru_paged_attn_decode(*d)
+    q = d[0].clone()
+    q[1, 2, 0] = float("nan")
+    got = rg.rglru_paged_attn_decode(q, *d[1:])
+    assert torch.isnan(got[1, 2]).all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(got[keep], out[keep])
 
 
 @pytest.mark.parametrize("io,dh", [("bf16", 128), ("f32", 64)])
