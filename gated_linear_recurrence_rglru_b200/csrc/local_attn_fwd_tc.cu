@@ -44,6 +44,8 @@ constexpr float kSlack = 8.0f;
 template <int DH> struct Cfg {
   static constexpr int kNQ = DH == 256 ? 1 : 2;          // query tiles of a block
   static constexpr int kNS = DH == 256 ? 2 : 1;          // score buffers of a query tile
+  static constexpr bool kApart = DH == 64;               // weights in columns of their own
+  static constexpr bool kAhead = kNS == 2 || kApart;     // S of a tile before P V of the last
   static constexpr int kCols = DH < 128 ? DH : 128;      // columns of a slot
   static constexpr int kPer = DH / kCols;                // slots of a tile
   static constexpr int kSlotBytes = kBN * kCols * 2;
@@ -55,11 +57,13 @@ template <int DH> struct Cfg {
   static constexpr int kThreads = (kSoftmax + 4) * 32;   // whole warp groups, for the register split
   static constexpr int kOffRing = kNQ * kQBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-  static constexpr int kNumBars = 2 * kSlots + 2 + kNQ * (2 * kNS + 3) + 1;
+  static constexpr int kNumBars = 2 * kSlots + 2 + kNQ * (3 * kNS + 4) + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMax = kOffMisc + 16;          // [2][2 groups][128 rows]
   static constexpr int kSmem = kOffMax + (kG == 2 ? 2 * 2 * kBM * 4 : 0);
-  static_assert(kSmem <= kMaxSmem && kNQ * (DH + kNS * kBN) <= 512, "shared memory, TMEM");
+  static constexpr int kOffS = kNQ * DH;                 // TMEM columns: O, scores, weights
+  static constexpr int kOffP = kOffS + kNQ * kNS * kBN;
+  static_assert(kSmem <= kMaxSmem && kOffP + (kApart ? kNQ * kBN / 2 : 0) <= 512, "shared memory, TMEM");
 };
 
 // The largest of N x 32 scores, in four chains.
@@ -155,11 +159,11 @@ __device__ __forceinline__ unsigned unit_at(unsigned r) {
 }
 
 // Ring fills of a unit in order of use: the K and V of tile i are fills
-// fill_of(i, is_v) .. + kPer - 1. One score buffer: K0 V0 K1 V1 ...; two: K0 K1 V0
-// K2 V1 ... K(n-1) V(n-2) V(n-1).
+// fill_of(i, is_v) .. + kPer - 1. K0 V0 K1 V1 ..., or, with the next scores ahead,
+// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
 template <int DH> __device__ __forceinline__ int fill_of(int i, bool is_v, int n) {
   using C = Cfg<DH>;
-  if (C::kNS == 1) return (2 * i + (is_v ? 1 : 0)) * C::kPer;
+  if (!C::kAhead) return (2 * i + (is_v ? 1 : 0)) * C::kPer;
   if (!is_v) return (i == 0 ? 0 : 2 * i - 1) * C::kPer;
   return (i + 1 < n ? 2 * i + 2 : 2 * i + 1) * C::kPer;
 }
@@ -183,11 +187,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   uint64_t *empty = full + C::kSlots;
   uint64_t *q_full = empty + C::kSlots, *q_empty = q_full + 1;
   uint64_t *s_full = q_empty + 1;                        // [kNQ][kNS]
-  uint64_t *p_full = s_full + C::kNQ * C::kNS;           // [kNQ][kNS]
-  uint64_t *o_done = p_full + C::kNQ * C::kNS;           // [kNQ] a tile's P V
+  uint64_t *p_full = s_full + C::kNQ * C::kNS;           // [halves][kNQ][kNS]
+  uint64_t *o_done = p_full + 2 * C::kNQ * C::kNS;       // [kNQ] a tile's P V
   uint64_t *all_done = o_done + C::kNQ;                  // [kNQ] a unit's last P V
   uint64_t *o_free = all_done + C::kNQ;                  // [kNQ] a unit's O was read
-  uint64_t *drained = o_free + C::kNQ;                   // used when a wait expired
+  uint64_t *s_free = o_free + C::kNQ;                    // [kNQ] scores apart from weights were read
+  uint64_t *drained = s_free + C::kNQ;                   // used when a wait expired
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + C::kOffMisc + 4);
   if (tid == 0) {
@@ -201,11 +206,13 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     for (int s = 0; s < C::kNQ * C::kNS; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4 * C::kG);
+      mbar_init(&p_full[C::kNQ * C::kNS + s], 4 * C::kG);
     }
     for (int q = 0; q < C::kNQ; ++q) {
       mbar_init(&o_done[q], 1);
       mbar_init(&all_done[q], 1);
       mbar_init(&o_free[q], 4 * C::kG);
+      mbar_init(&s_free[q], 4 * C::kG);
     }
     *abort = 0;
     fence_mbar_init();
@@ -300,7 +307,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     // S of query tile q and key tile i; `last`: the tile's K has no later reader
     auto scores = [&](const Un &un, int q, int i, bool last) {
       const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[q] % C::kNS;
-      const uint32_t d = tmem + C::kNQ * DH + sb * kBN;
+      const uint32_t d = tmem + C::kOffS + sb * kBN;
+      if (C::kApart && js[q] > 0 && !wait(&s_free[q], (js[q] - 1) & 1)) return;
       for (int x = 0; x < C::kPer; ++x) {
         const int s = (f + x) % C::kSlots;
         if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
@@ -324,28 +332,37 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       ++js[q];
     };
-    // O of query tile q gains P V of key tile i; `first`, `done`: of the unit
+    // O of query tile q gains P V of key tile i, in the two halves in which the
+    // softmax warps hand the weights over; `first`, `done`: of the unit
     auto values = [&](const Un &un, int q, int i, bool first, bool done, bool last) {
       const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[q] % C::kNS;
-      if (!wait(&p_full[sb], (jp[q] / C::kNS) & 1)) return;
+      const uint32_t a = tmem + (C::kApart ? C::kOffP + q * (kBN / 2) : C::kOffS + sb * kBN);
       if (first && nu[q] > 0 && !wait(&o_free[q], (nu[q] - 1) & 1)) return;
-      const uint32_t a = tmem + C::kNQ * DH + sb * kBN;
-      for (int x = 0; x < C::kPer; ++x) {
-        const int s = (f + x) % C::kSlots;
-        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
-        const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
-        if (elect_one()) {
+      for (int x = 0; x < C::kPer; ++x)
+        if (!wait(&full[(f + x) % C::kSlots], ((f + x) / C::kSlots) & 1)) return;
+      for (int half = 0; half < 2; ++half) {
+        if (!wait(&p_full[half * C::kNQ * C::kNS + sb], (jp[q] / C::kNS) & 1)) return;
+        for (int x = 0; x < C::kPer; ++x) {
+          const int s = (f + x) % C::kSlots;
+          const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBN / 16; ++k)
-            mma_ts(tmem + q * DH + x * C::kCols, a + (C::kG == 2 ? (k >> 2) * 64 + (k & 3) * 8 : k * 8), bd + ((k * 16 * 128) >> 4),
-                   id_o, k > 0 ? 1u : !first);
-          if (last) mma_commit(&empty[s]);
-          if (x == C::kPer - 1) {
-            mma_commit(&o_done[q]);
-            if (done) mma_commit(&all_done[q]);
+            for (int k = 0; k < kBN / 32; ++k) {
+              // the first half of each group's columns, then the second
+              const int ks = C::kG == 2 ? (k >> 1) * 4 + half * 2 + (k & 1) : half * 4 + k;
+              mma_ts(tmem + q * DH + x * C::kCols, a + (C::kG == 2 ? (ks >> 2) * 64 + (ks & 3) * 8 : ks * 8),
+                     bd + ((ks * 16 * 128) >> 4), id_o, half + k > 0 ? 1u : !first);
+            }
+            if (half == 1) {
+              if (last) mma_commit(&empty[s]);
+              if (x == C::kPer - 1) {
+                mma_commit(&o_done[q]);
+                if (done) mma_commit(&all_done[q]);
+              }
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       ++jp[q];
     };
@@ -372,12 +389,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           const bool now1 = i >= 0 && un.sees(p, 1, i), next1 = i + 1 < n && un.sees(p, 1, i + 1);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            if (ok && (q == 1 ? now1 : i >= 0 && un.sees(p, 0, i))) {
+            const bool now = q == 1 ? now1 : i >= 0 && un.sees(p, 0, i);
+            const bool next = q == 1 ? next1 : i + 1 < n && un.sees(p, 0, i + 1);
+            if (C::kAhead && ok && next) scores(un, q, i + 1, q == 1 || !next1);
+            if (ok && now) {
               values(un, q, i, !begun[q], i == end[q], q == 1 || !now1);
               begun[q] = true;
             }
-            if (ok && (q == 1 ? next1 : i + 1 < n && un.sees(p, 0, i + 1)))
-              scores(un, q, i + 1, q == 1 || !next1);
+            if (!C::kAhead && ok && next) scores(un, q, i + 1, q == 1 || !next1);
           }
         }
         nu[0] += begun[0] ? 1 : 0;
@@ -399,7 +418,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const int q = C::kNQ == 2 ? warp >> 2 : 0, g = C::kG == 2 ? warp >> 2 : 0, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lanes + q * DH + g * kOut;
-    const uint32_t t_s = tmem + lanes + C::kNQ * DH + q * C::kNS * kBN + g * kCols;
+    const uint32_t t_s = tmem + lanes + C::kOffS + q * C::kNS * kBN + g * kCols;
     float *shared_max = reinterpret_cast<float *>(sm + C::kOffMax);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
     bool ok = true;                  // a warp whose wait expired still meets the block barriers
@@ -431,6 +450,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         begun = true;
         const int s = j % C::kNS, k0 = un.kt.tile(i) * kBN;
         const uint32_t ts = t_s + s * kBN;
+        const uint32_t tp = C::kApart ? tmem + lanes + C::kOffP + q * (kBN / 2) : ts;
         // Where every query of the tile sees every key of it, the scores stay in
         // registers from the maximum to the weights. Elsewhere they are read twice, 32
         // columns at a time in rolled loops (unrolled over a row, that path alone
@@ -443,6 +463,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           const int lo = p.window > 0 ? t + off - p.window + 1 - key : 0;
           return bits_between(lo, hi) | bits_between(0, min(hi, p.sinks - key - 1));
         };
+        // the scores' columns may take the next tile's (where weights lie apart from them)
+        auto read = [&]() {
+          if constexpr (C::kApart) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[q]);
+          }
+        };
         float v[kCols / 32][32], top = -INFINITY;
         if (wait(&s_full[q * C::kNS + s], (j / C::kNS) & 1)) {
           if (whole) {
@@ -450,6 +478,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + c * 32, v[c]);
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) tmem_wait_ld32(v[c]);
+            read();
             top = max_of(v);
           } else {
 #pragma unroll 1
@@ -491,35 +520,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             tmem_wait_st();
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
-        const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-base, -base);
-        unsigned long long sum[2] = {0ull, 0ull};
-        // the weights of a group's columns go to the first half of its score columns
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
-            uint32_t packed[16];
-            weights32<C::kPoly>(v[c], cc, mm, sum, packed);
-            tmem_st16u(ts + c * 16, packed);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kCols; c += 32) {
-            const uint32_t bits = seen(c);
-            uint32_t packed[16] = {};
-            if (C::kG == 2 || __any_sync(0xFFFFFFFFu, bits != 0u)) {
-              float w[32];
-              tmem_ld32(ts + c, w);
-              tmem_wait_ld32(w);
-              hide(w, bits, -INFINITY);
-              weights32<0>(w, cc, mm, sum, packed);      // hidden scores give 0 exactly
-            }
-            tmem_st16u(ts + c / 2, packed);
-          }
-        }
-        float s0, s1;
-        unpair(add2(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
         const DeadKeys dead = dead_keys(p, un.n.nk);
         if (dead.any(k0, kBN)) {
           // zero the value rows that no query sees, once V is there (each query tile
@@ -535,10 +535,49 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&p_full[q * C::kNS + s]);
+        if (C::kApart && !first) wait(&o_done[q], (j - 1) & 1);   // the last tile's weights were read
+        // half of the thread's weights are in TMEM: the tensor core may use them
+        auto publish = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&p_full[(half * C::kNQ + q) * C::kNS + s]);
+        };
+        const float base = m == -INFINITY ? 0.0f : m;
+        const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-base, -base);
+        unsigned long long sum[2] = {0ull, 0ull};
+        // The weights of a group's columns go to the first half of its score columns,
+        // or to columns of their own. The first half of them is handed over when the
+        // next 32 are computed, so that its stores have long ended.
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t packed[16];
+            weights32<C::kPoly>(v[c], cc, mm, sum, packed);
+            if (c == kCols / 64) publish(0);
+            tmem_st16u(tp + c * 16, packed);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += 32) {
+            const uint32_t bits = seen(c);
+            uint32_t packed[16] = {};
+            if (C::kG == 2 || __any_sync(0xFFFFFFFFu, bits != 0u)) {
+              float w[32];
+              tmem_ld32(ts + c, w);
+              tmem_wait_ld32(w);
+              hide(w, bits, -INFINITY);
+              weights32<0>(w, cc, mm, sum, packed);      // hidden scores give 0 exactly
+            }
+            if (c == kCols / 2) publish(0);
+            tmem_st16u(tp + c / 2, packed);
+          }
+          read();
+        }
+        publish(1);
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         ++j;
       }
       f0 += 2 * un.kt.n * C::kPer;
