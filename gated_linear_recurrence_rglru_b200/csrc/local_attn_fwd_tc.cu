@@ -8,8 +8,8 @@
 // head and the key tiles that their mask leaves, the next unit's copies and first
 // scores running while the softmax warps store the last one's rows. Heads 64 and
 // 128 wide: a block works on two query tiles at once, which share every K and V
-// tile (two heads of a group, or two tiles of one head), and take turns: while the
-// softmax works on one's scores, the tensor core does the other's P V and next S.
+// tile (two heads of a group, or two tiles of one head): while the softmax
+// works on one's scores, the tensor core does the other's P V and next S.
 // 256 wide: one query tile (O takes 256 TMEM columns) with two score buffers, S of
 // the next key tile is made while the softmax works on this one.
 //
@@ -46,6 +46,7 @@ template <int DH> struct Cfg {
   static constexpr int kNS = DH == 256 ? 2 : 1;          // score buffers of a query tile
   static constexpr bool kApart = DH == 64;               // weights in columns of their own
   static constexpr bool kAhead = kNS == 2 || kApart;     // S of a tile before P V of the last
+  static constexpr int kIssuers = DH == 64 ? 2 : 1;      // warps that issue MMAs
   static constexpr int kCols = DH < 128 ? DH : 128;      // columns of a slot
   static constexpr int kPer = DH / kCols;                // slots of a tile
   static constexpr int kSlotBytes = kBN * kCols * 2;
@@ -57,7 +58,7 @@ template <int DH> struct Cfg {
   static constexpr int kThreads = (kSoftmax + 4) * 32;   // whole warp groups, for the register split
   static constexpr int kOffRing = kNQ * kQBytes;
   static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-  static constexpr int kNumBars = 2 * kSlots + 2 + kNQ * (3 * kNS + 4) + 1;
+  static constexpr int kNumBars = 2 * kSlots + kNQ * (3 * kNS + 6) + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMax = kOffMisc + 16;          // [2][2 groups][128 rows]
   static constexpr int kSmem = kOffMax + (kG == 2 ? 2 * 2 * kBM * 4 : 0);
@@ -104,7 +105,7 @@ __device__ __forceinline__ void weights32(const float (&v)[32], unsigned long lo
 struct Params {
   AttnArgs a;
   int n_qt;        // query tiles of a row; pairs of them when `rows2`
-  int n_h;         // heads of a row; pairs of them when a block's two tiles are two heads
+  unsigned n_h;    // heads of a row; pairs of them when a block's two tiles are two heads
   int rows2;       // a block's two query tiles follow each other in one head
   unsigned units;
   int v8;          // out rows may be stored 32 bytes at a time
@@ -123,10 +124,10 @@ template <int NQ> struct Unit {
   __device__ Unit(const Params &prm, unsigned u) {
     const AttnArgs &p = prm.a;
     rows2 = NQ == 2 ? prm.rows2 : 0;
-    h = static_cast<int>(u % static_cast<unsigned>(prm.n_h)) * (NQ == 2 && !rows2 ? 2 : 1);
-    const unsigned rest = u / static_cast<unsigned>(prm.n_h);
-    b = static_cast<int>(rest % static_cast<unsigned>(p.B));
-    q0 = (prm.n_qt - 1 - static_cast<int>(rest / static_cast<unsigned>(p.B))) * kBM * (1 + rows2);
+    const unsigned rest = u / prm.n_h, far = rest / static_cast<unsigned>(p.B);
+    h = static_cast<int>(u - rest * prm.n_h) * (NQ == 2 && !rows2 ? 2 : 1);
+    b = static_cast<int>(rest - far * static_cast<unsigned>(p.B));
+    q0 = (prm.n_qt - 1 - static_cast<int>(far)) * kBM * (1 + rows2);
     n = row_lens(p, b);
     kt = {0, 0, 0};
     if (q0 < n.nq)
@@ -185,8 +186,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const int off = p.S - p.T;
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
   uint64_t *empty = full + C::kSlots;
-  uint64_t *q_full = empty + C::kSlots, *q_empty = q_full + 1;
-  uint64_t *s_full = q_empty + 1;                        // [kNQ][kNS]
+  uint64_t *q_full = empty + C::kSlots, *q_empty = q_full + C::kNQ;      // [kNQ]
+  uint64_t *s_full = q_empty + C::kNQ;                   // [kNQ][kNS]
   uint64_t *p_full = s_full + C::kNQ * C::kNS;           // [halves][kNQ][kNS]
   uint64_t *o_done = p_full + 2 * C::kNQ * C::kNS;       // [kNQ] a tile's P V
   uint64_t *all_done = o_done + C::kNQ;                  // [kNQ] a unit's last P V
@@ -198,17 +199,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], C::kIssuers);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(drained, 1);
+    mbar_init(drained, C::kIssuers);
     for (int s = 0; s < C::kNQ * C::kNS; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4 * C::kG);
       mbar_init(&p_full[C::kNQ * C::kNS + s], 4 * C::kG);
     }
     for (int q = 0; q < C::kNQ; ++q) {
+      mbar_init(&q_full[q], 1);
+      mbar_init(&q_empty[q], 1);
       mbar_init(&o_done[q], 1);
       mbar_init(&all_done[q], 1);
       mbar_init(&o_free[q], 4 * C::kG);
@@ -240,7 +241,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (warp == kTma) {
     // ============================ TMA producer ============================
     if (lane == 0) {
-      int f = 0, nu = 0;                                 // fills and units issued
+      int f = 0, nu[2] = {0, 0};                         // fills and query tiles issued
       bool ok = true;
       for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
         const Un un(prm, u);
@@ -266,36 +267,44 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                           &full[s], x * C::kCols + c * 64, un.kt.tile(i) * kBN, kvh, un.b);
           }
           if (ok && !is_v && i == 0) {
-            if (!mbar_wait(q_empty, (nu & 1) ^ 1, abort, kWaitNs)) {
-              give_up();
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(q_full, C::kNQ * C::kQBytes);
-            for (int q = 0; q < C::kNQ; ++q)
+            for (int q = 0; q < C::kNQ && ok; ++q) {
+              if (!mbar_wait(&q_empty[q], (nu[q] & 1) ^ 1, abort, kWaitNs)) {
+                give_up();
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(&q_full[q], C::kQBytes);
               for (int c = 0; c < DH / 64; ++c)
-                tma_load_4d(sm + q * C::kQBytes + c * (kBM * 128), &tmap_q, q_full, c * 64, un.first(q),
+                tma_load_4d(sm + q * C::kQBytes + c * (kBM * 128), &tmap_q, &q_full[q], c * 64, un.first(q),
                             un.head(q), un.b);
-            ++nu;
+              ++nu[q];
+            }
           }
         }
       }
       if (*abort) {
-        if (nu > 0) mbar_wait_drain(q_full, (nu - 1) & 1, kDrainNs);
+        for (int q = 0; q < C::kNQ; ++q)
+          if (nu[q] > 0) mbar_wait_drain(&q_full[q], (nu[q] - 1) & 1, kDrainNs);
         for (int j = f - 1; j >= 0 && j >= f - C::kSlots; --j)
           mbar_wait_drain(&full[j % C::kSlots], (j / C::kSlots) & 1, kDrainNs);
       }
     }
-  } else if (warp == kMma) {
-    // ============================= MMA issuer =============================
-    // The whole warp walks, one elected lane issues.
+  } else if (warp < kMma + C::kIssuers) {
+    // ============================ MMA issuers =============================
+    // The whole warp walks, one elected lane issues. 64 wide, where the softmax
+    // takes longer than the tensor core, each query tile has a warp of its own, so
+    // that neither waits for the other's (batch of short windows: 31 -> 27 us). 128
+    // wide, one warp takes turns with the two: on their own, both would want the
+    // tensor core at once and the softmax units at once (128 -> 153 us on 8192
+    // tokens, 16 heads).
+    constexpr int kMine = C::kNQ / C::kIssuers;          // query tiles of this warp
     constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
     constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
     const uint32_t base = smem_u32(sm);
+    const int first_q = warp - kMma;
     bool ok = true;
-    int f0 = 0;                                          // fills before this unit
-    int units = 0;                                       // units before this one
-    int js[2] = {0, 0}, jp[2] = {0, 0}, nu[2] = {0, 0};  // tiles scored, tiles added, units, by query tile
+    int f0 = 0, units = 0;                               // fills and units before this unit
+    int js[kMine] = {}, jp[kMine] = {}, nu[kMine] = {};  // tiles scored, tiles added, units with a key
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
         give_up();
@@ -304,11 +313,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) tc_fence_after();
       return ok;
     };
-    // S of query tile q and key tile i; `last`: the tile's K has no later reader
-    auto scores = [&](const Un &un, int q, int i, bool last) {
-      const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[q] % C::kNS;
+    // a tile that this warp's query tiles do not see: its slots are the other warp's alone
+    auto pass = [&](int f) {
+      for (int x = 0; kMine == 1 && x < C::kPer; ++x) {  // (of two, one sees it)
+        const int s = (f + x) % C::kSlots;
+        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
+        if (elect_one()) mbar_arrive(&empty[s]);
+        __syncwarp();
+      }
+    };
+    // S of key tile i; `last`: Q has no later reader; `free`: nor has K, of this warp
+    auto scores = [&](const Un &un, int y, int i, bool last, bool free) {
+      const int q = first_q + y;
+      const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[y] % C::kNS;
       const uint32_t d = tmem + C::kOffS + sb * kBN;
-      if (C::kApart && js[q] > 0 && !wait(&s_free[q], (js[q] - 1) & 1)) return;
+      if (C::kApart && js[y] > 0 && !wait(&s_free[q], (js[y] - 1) & 1)) return;
       for (int x = 0; x < C::kPer; ++x) {
         const int s = (f + x) % C::kSlots;
         if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
@@ -322,26 +341,27 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const uint32_t o = ((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4;
             mma_ss(d, ad + o, bd + o, id_s, k > 0 ? 1u : x > 0);
           }
-          if (last) mma_commit(&empty[s]);
+          if (free) mma_commit(&empty[s]);
           if (x == C::kPer - 1) {
             mma_commit(&s_full[sb]);
-            if (last && i == un.kt.n - 1) mma_commit(q_empty);
+            if (last) mma_commit(&q_empty[q]);
           }
         }
         __syncwarp();
       }
-      ++js[q];
+      ++js[y];
     };
-    // O of query tile q gains P V of key tile i, in the two halves in which the
-    // softmax warps hand the weights over; `first`, `done`: of the unit
-    auto values = [&](const Un &un, int q, int i, bool first, bool done, bool last) {
-      const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[q] % C::kNS;
+    // O gains P V of key tile i, in the two halves in which the softmax warps hand
+    // the weights over; `first`, `done`: of the unit
+    auto values = [&](const Un &un, int y, int i, bool first, bool done, bool free) {
+      const int q = first_q + y;
+      const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[y] % C::kNS;
       const uint32_t a = tmem + (C::kApart ? C::kOffP + q * (kBN / 2) : C::kOffS + sb * kBN);
-      if (first && nu[q] > 0 && !wait(&o_free[q], (nu[q] - 1) & 1)) return;
+      if (first && nu[y] > 0 && !wait(&o_free[q], (nu[y] - 1) & 1)) return;
       for (int x = 0; x < C::kPer; ++x)
         if (!wait(&full[(f + x) % C::kSlots], ((f + x) / C::kSlots) & 1)) return;
       for (int half = 0; half < 2; ++half) {
-        if (!wait(&p_full[half * C::kNQ * C::kNS + sb], (jp[q] / C::kNS) & 1)) return;
+        if (!wait(&p_full[half * C::kNQ * C::kNS + sb], (jp[y] / C::kNS) & 1)) return;
         for (int x = 0; x < C::kPer; ++x) {
           const int s = (f + x) % C::kSlots;
           const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
@@ -354,7 +374,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                      bd + ((ks * 16 * 128) >> 4), id_o, half + k > 0 ? 1u : !first);
             }
             if (half == 1) {
-              if (last) mma_commit(&empty[s]);
+              if (free) mma_commit(&empty[s]);
               if (x == C::kPer - 1) {
                 mma_commit(&o_done[q]);
                 if (done) mma_commit(&all_done[q]);
@@ -364,44 +384,46 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           __syncwarp();
         }
       }
-      ++jp[q];
+      ++jp[y];
     };
     for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
       const Un un(prm, u);
       const int n = un.kt.n;
       if (n == 0) continue;
-      wait(q_full, units & 1);
-      ++units;
-      if constexpr (C::kNQ == 1) {
-        if (ok) scores(un, 0, 0, true);
-        for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n) scores(un, 0, i + 1, true);
-          if (ok) values(un, 0, i, i == 0, i == n - 1, true);
-        }
-        ++nu[0];
-      } else {
-        // the two query tiles take turns: while the softmax works on one's scores,
-        // the other's P V and next S run. A tile of one that sees none of the keys
-        // is passed over; its part in releasing the slots falls to the other.
-        const int end[2] = {un.last(p, 0), un.last(p, 1)};
-        bool begun[2] = {false, false};
-        for (int i = -1; i < n && ok; ++i) {
-          const bool now1 = i >= 0 && un.sees(p, 1, i), next1 = i + 1 < n && un.sees(p, 1, i + 1);
+      int end[kMine];                                    // the last tile that each sees
+      bool begun[kMine] = {};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const bool now = q == 1 ? now1 : i >= 0 && un.sees(p, 0, i);
-            const bool next = q == 1 ? next1 : i + 1 < n && un.sees(p, 0, i + 1);
-            if (C::kAhead && ok && next) scores(un, q, i + 1, q == 1 || !next1);
-            if (ok && now) {
-              values(un, q, i, !begun[q], i == end[q], q == 1 || !now1);
-              begun[q] = true;
-            }
-            if (!C::kAhead && ok && next) scores(un, q, i + 1, q == 1 || !next1);
-          }
+      for (int y = 0; y < kMine; ++y) {
+        wait(&q_full[first_q + y], units & 1);
+        end[y] = un.last(p, first_q + y);
+        if (end[y] < 0 && ok) {                          // none: Q is not read
+          if (elect_one()) mbar_arrive(&q_empty[first_q + y]);
+          __syncwarp();
         }
-        nu[0] += begun[0] ? 1 : 0;
-        nu[1] += begun[1] ? 1 : 0;
       }
+      ++units;
+      auto next = [&](int y, int i) {
+        if (!ok || i >= n) return;
+        if (un.sees(p, first_q + y, i)) scores(un, y, i, i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
+        else pass(f0 + fill_of<DH>(i, false, n));
+      };
+      for (int i = -1; i < n && ok; ++i) {
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) {
+          if (C::kAhead) next(y, i + 1);
+          if (ok && i >= 0) {
+            if (un.sees(p, first_q + y, i)) {
+              values(un, y, i, !begun[y], i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
+              begun[y] = true;
+            } else {
+              pass(f0 + fill_of<DH>(i, true, n));
+            }
+          }
+          if (!C::kAhead) next(y, i + 1);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) nu[y] += begun[y] ? 1 : 0;
       f0 += 2 * n * C::kPer;
     }
     if (*abort) {                                        // let what was issued finish
@@ -444,6 +466,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const long long lse_row = (static_cast<long long>(un.b) * p.Hq + un.head(q)) * p.T + t;
       float m = -INFINITY, l = 0.0f;
       bool begun = false;
+      const DeadKeys dead = dead_keys(p, un.n.nk);
       for (int i = 0; i < un.kt.n; ++i) {
         if (!un.sees(p, q, i)) continue;
         const bool first = !begun;
@@ -520,7 +543,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             tmem_wait_st();
           }
         }
-        const DeadKeys dead = dead_keys(p, un.n.nk);
         if (dead.any(k0, kBN)) {
           // zero the value rows that no query sees, once V is there (each query tile
           // does, before its own product: zeros over zeros)
@@ -647,7 +669,7 @@ template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
   prm.a = p;
   prm.rows2 = C::kNQ == 2 && (p.Hq / p.Hkv) % 2 != 0 ? 1 : 0;
   prm.n_qt = ceil_div(p.T, kBM * (1 + prm.rows2));
-  prm.n_h = C::kNQ == 2 && !prm.rows2 ? p.Hq / 2 : p.Hq;
+  prm.n_h = static_cast<unsigned>(C::kNQ == 2 && !prm.rows2 ? p.Hq / 2 : p.Hq);
   prm.units = static_cast<unsigned>(static_cast<long long>(prm.n_qt) * p.B * prm.n_h);
   prm.v8 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 ? 1 : 0;
   prm.c = p.scale * kLog2e;

@@ -562,7 +562,17 @@ template <typename T> cudaError_t bwd_typed(const AttnArgs &p, void *ws, cudaStr
   return launch_attn_join(p, sizeof(T) == 4 ? RGLRU_IO_F32 : RGLRU_IO_BF16, pl, parts, st);
 }
 
+// Tiles of 64 queries, fewer where the operands of wide heads leave no room; 32 of
+// heads up to 128 wide when there are fewer tiles of 64 than SMs (fp32, 2 x 500
+// queries, 4 heads of 64, window 256: 42 us with 64, 30 with 32; 192 wide 32 take
+// as long as 48).
 template <typename T> cudaError_t fwd_typed(const AttnArgs &p, cudaStream_t st) {
+  const bool few = static_cast<long long>(p.B) * p.Hq * ceil_div(p.T, 64) < 148;
+  switch (ceil_div(p.dh, 64)) {
+    case 1: if (few) return run_fwd<T, 32, 1>(p, st); break;
+    case 2: if (few) return run_fwd<T, 32, 2>(p, st); break;
+    default: break;
+  }
   switch (ceil_div(p.dh, 64)) {
     case 1: return run_fwd<T, 64, 1>(p, st);
     case 2: return run_fwd<T, 64, 2>(p, st);
