@@ -28,6 +28,7 @@
 // Every wait is bounded; on expiry the kernel records RGLRU_ERR_TIMEOUT (wait
 // site 7), drains what it issued and returns.
 #include "attn_tc.cuh"
+#include "tc_pair.cuh"
 
 namespace rglru {
 namespace {
@@ -40,6 +41,7 @@ constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSite = 7;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
+constexpr int kLeast = 2;                                // key tiles of a part of a unit
 
 template <int DH> struct Cfg {
   static constexpr int kNQ = DH == 256 ? 1 : 2;          // query tiles of a block
@@ -108,6 +110,7 @@ struct Params {
   unsigned n_h;    // heads of a row; pairs of them when a block's two tiles are two heads
   int rows2;       // a block's two query tiles follow each other in one head
   unsigned units;
+  int parts;       // blocks of a cluster that share a unit's key tiles (kSplit)
   int v8;          // out rows may be stored 32 bytes at a time
   float c;         // scale * log2 e
 };
@@ -117,8 +120,9 @@ struct Params {
 // where heads are odd in a group, two tiles of one head. Heads fastest (they share
 // keys), then rows, then query tiles from the last (the longest walks of an
 // unwindowed causal mask come first).
-template <int NQ> struct Unit {
-  int h, b, q0, rows2;
+// kSplit: the part-th of prm.parts shares of the unit's key tiles.
+template <int NQ, bool kSplit> struct Unit {
+  int h, b, q0, rows2, first_tile;
   RowLens n;
   KeyTiles kt;
   __device__ Unit(const Params &prm, unsigned u) {
@@ -133,13 +137,21 @@ template <int NQ> struct Unit {
     if (q0 < n.nq)
       kt = key_tiles(q0 + p.S - p.T, min(q0 + kBM * (1 + rows2), n.nq) - 1 + p.S - p.T, n.nk, p.window,
                      p.sinks, kBN);
+    if constexpr (kSplit) {
+      const int part = static_cast<int>(blockIdx.x) % prm.parts;
+      first_tile = kt.n * part / prm.parts;
+      kt.n = kt.n * (part + 1) / prm.parts - first_tile;
+      kt.win += max(first_tile - kt.sink_end, 0);
+      kt.sink_end = max(kt.sink_end - first_tile, 0);
+    }
   }
+  __device__ int tile(int i) const { return (kSplit && i < kt.sink_end ? first_tile : 0) + kt.tile(i); }
   __device__ int head(int q) const { return h + (NQ == 2 && !rows2 ? q : 0); }
   __device__ int first(int q) const { return q0 + (NQ == 2 && rows2 ? q * kBM : 0); }
   // whether any query of tile q sees any key of key tile i
   __device__ bool sees(const AttnArgs &p, int q, int i) const {
     if (NQ == 1 || !rows2) return true;
-    const int f = first(q), off = p.S - p.T, k0 = kt.tile(i) * kBN;
+    const int f = first(q), off = p.S - p.T, k0 = tile(i) * kBN;
     return f < n.nq && k0 <= min(f + kBM, n.nq) - 1 + off &&
            (p.window == 0 || k0 + kBN - 1 > f + off - p.window || k0 < p.sinks);
   }
@@ -148,6 +160,11 @@ template <int NQ> struct Unit {
     if (NQ == 1 || !rows2) return kt.n - 1;
     const int f = first(q), hi = min(min(f + kBM, n.nq) - 1 + p.S - p.T, n.nk - 1);
     if (f >= n.nq || hi < 0) return -1;
+    if constexpr (kSplit) {
+      int x = kt.n - 1;
+      while (x >= 0 && !sees(p, q, x)) --x;
+      return x;
+    }
     const int x = hi / kBN;
     return x < kt.win ? x : kt.sink_end + x - kt.win;
   }
@@ -155,7 +172,8 @@ template <int NQ> struct Unit {
 
 // The block's r-th unit: units come sorted by length, and every second round runs
 // backwards over the blocks, so that their sums stay close.
-__device__ __forceinline__ unsigned unit_at(unsigned r) {
+template <bool kSplit> __device__ __forceinline__ unsigned unit_at(const Params &prm, unsigned r) {
+  if (kSplit) return r == 0 ? blockIdx.x / static_cast<unsigned>(prm.parts) : prm.units;
   return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
 }
 
@@ -169,12 +187,105 @@ template <int DH> __device__ __forceinline__ int fill_of(int i, bool is_v, int n
   return (i + 1 < n ? 2 * i + 2 : 2 * i + 1) * C::kPer;
 }
 
-template <int DH>
+// The parts of a split unit to its rows: every block of the cluster leaves O (not
+// divided yet), m and l of its keys in its shared memory, where the operands were, and
+// each joins its share of the rows (half of them at most) from all, in the order of the parts:
+//   M = max m_i,  f_i = 2^(m_i - M),  L = sum l_i f_i,  out = sum O_i f_i / L
+template <int DH, typename Un>
+__device__ __forceinline__ void join(const Params &prm, const Un &un, uint32_t t_o, bool some, int q, int g,
+                                     int row, float m, float l, unsigned char *sm) {
+  using C = Cfg<DH>;
+  constexpr int kPitch = DH + 4, kOut = DH / C::kG, kRows = C::kNQ * kBM;
+  static_assert(kRows * (kPitch + 2 + 4) * 4 <= C::kOffBar, "the parts' room");
+  const AttnArgs &p = prm.a;
+  float *part = reinterpret_cast<float *>(sm), *ml = part + kRows * kPitch, *fs = ml + 2 * kRows;
+  asm volatile("bar.sync 2, 256;" ::: "memory");         // no product of the block reads its operands now
+  const int at = q * kBM + row;
+  if (some) {
+#pragma unroll 1
+    for (int c = 0; c < kOut; c += 32) {
+      float o[32];
+      tmem_ld32(t_o + c, o);
+      tmem_wait_ld32(o);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4 *>(part + at * kPitch + g * kOut + c + e) =
+            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+  }
+  if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * at) = make_float2(m, some ? l : 0.0f);
+  cluster_sync();
+  const int tid = threadIdx.x, parts = prm.parts, share = kRows / parts;
+  const int x0 = static_cast<int>(cluster_ctarank()) * share;            // this block's rows
+  const uint32_t mine = smem_u32(part);
+  if (tid < share) {                                     // f_i / L of a row
+    const int x = x0 + tid, y = x / kBM, t = un.first(y) + x % kBM;
+    float pm[8], pl[8], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pm[i] = -INFINITY;
+      pl[i] = 0.0f;
+      if (i < parts) ld_cluster(mapa_shared(mine + (kRows * kPitch + 2 * x) * 4, i), pm[i], pl[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (pl[i] != 0.0f) top = fmaxf(top, pm[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pm[i] = pl[i] == 0.0f ? 0.0f : ex2(pm[i] - top);
+      sum += pl[i] * pm[i];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fs[tid * 8 + i] = pl[i] == 0.0f ? 0.0f : pm[i] * inv;
+    if (t < un.n.nq && p.lse != nullptr)
+      p.lse[(static_cast<long long>(un.b) * p.Hq + un.head(y)) * p.T + t] =
+          sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+  }
+  asm volatile("bar.sync 2, 256;" ::: "memory");
+  constexpr int kV = DH / 4, kN = 4;                     // 16-byte pieces of a row; at once of a thread
+  for (int z = tid; z < share * kV; z += 256 * kN) {
+    float4 acc[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int i = 0; i < parts; ++i) {
+      const uint32_t from = mapa_shared(mine, i);
+      float4 o[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const int w = min(z + e * 256, share * kV - 1);
+        o[e] = ld_cluster4(from + ((x0 + w / kV) * kPitch + w % kV * 4) * 4);
+      }
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const float f = fs[min(z + e * 256, share * kV - 1) / kV * 8 + i];
+        if (f != 0.0f) {                                 // (else what lies there may not be O)
+          acc[e].x = fmaf(o[e].x, f, acc[e].x);
+          acc[e].y = fmaf(o[e].y, f, acc[e].y);
+          acc[e].z = fmaf(o[e].z, f, acc[e].z);
+          acc[e].w = fmaf(o[e].w, f, acc[e].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const int w = z + e * 256, x = x0 + w / kV, y = x / kBM, t = un.first(y) + x % kBM;
+      if (w < share * kV && t < un.n.nq)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                   ((static_cast<long long>(un.b) * p.T + t) * p.Hq + un.head(y)) * DH +
+                                   w % kV * 4) = make_uint2(bf16x2(acc[e].x, acc[e].y), bf16x2(acc[e].z, acc[e].w));
+    }
+  }
+  cluster_sync();                                        // the others have read this block's part
+}
+
+template <int DH, bool kSplit>
 __global__ void __launch_bounds__(Cfg<DH>::kThreads, 1)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Params prm) {
   using C = Cfg<DH>;
-  using Un = Unit<C::kNQ>;
+  using Un = Unit<C::kNQ, kSplit>;
   constexpr int kTma = C::kSoftmax, kMma = C::kSoftmax + 1;       // warps
   extern __shared__ __align__(1024) unsigned char sm[];
   const AttnArgs &p = prm.a;
@@ -243,7 +354,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (lane == 0) {
       int f = 0, nu[2] = {0, 0};                         // fills and query tiles issued
       bool ok = true;
-      for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
+      for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
         const Un un(prm, u);
         if (un.kt.n == 0) continue;
         const int kvh = un.h / (p.Hq / p.Hkv);
@@ -264,7 +375,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             mbar_arrive_expect_tx(&full[s], C::kSlotBytes);
             for (int c = 0; c < C::kCols / 64; ++c)
               tma_load_4d(sm + C::kOffRing + s * C::kSlotBytes + c * (kBN * 128), is_v ? &tmap_v : &tmap_k,
-                          &full[s], x * C::kCols + c * 64, un.kt.tile(i) * kBN, kvh, un.b);
+                          &full[s], x * C::kCols + c * 64, un.tile(i) * kBN, kvh, un.b);
           }
           if (ok && !is_v && i == 0) {
             for (int q = 0; q < C::kNQ && ok; ++q) {
@@ -386,7 +497,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       ++jp[y];
     };
-    for (unsigned r = 0, u; (u = unit_at(r)) < prm.units && ok; ++r) {
+    for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
       const Un un(prm, u);
       const int n = un.kt.n;
       if (n == 0) continue;
@@ -459,7 +570,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       bar_sync_softmax<256>();
       return shared_max[(buffer * 2 + (g ^ 1)) * kBM + row];
     };
-    for (unsigned r = 0, u; (u = unit_at(r)) < prm.units; ++r) {
+    for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units; ++r) {
       const Un un(prm, u);
       const int q0 = un.first(q), t = q0 + row;
       const long long out_row = (static_cast<long long>(un.b) * p.T + t) * p.Hq + un.head(q);
@@ -471,7 +582,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (!un.sees(p, q, i)) continue;
         const bool first = !begun;
         begun = true;
-        const int s = j % C::kNS, k0 = un.kt.tile(i) * kBN;
+        const int s = j % C::kNS, k0 = un.tile(i) * kBN;
         const uint32_t ts = t_s + s * kBN;
         const uint32_t tp = C::kApart ? tmem + lanes + C::kOffP + q * (kBN / 2) : ts;
         // Where every query of the tile sees every key of it, the scores stay in
@@ -602,6 +713,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         l += s0 + s1;
         ++j;
       }
+      if constexpr (kSplit) {
+        if (begun) wait(&all_done[q], 0);
+        if (C::kG == 2) l += exchange(l, j & 1);
+        join<DH>(prm, un, t_o, ok && begun, q, g, row, m, l, sm);
+        break;
+      }
       f0 += 2 * un.kt.n * C::kPer;
       const bool live = t < un.n.nq;
       if (!begun) {                                      // sees no key
@@ -650,21 +767,77 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       ++nu;
     }
   }
+  if constexpr (kSplit) {
+    if (warp >= kTma) {                                  // the softmax warps' barriers of join
+      cluster_sync();
+      cluster_sync();
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
+template <int DH> cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *attr, unsigned parts, unsigned units) {
+  using C = Cfg<DH>;
+  cudaLaunchConfig_t cfg = {};
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = parts;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.gridDim = dim3(units * parts);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of 2 << x blocks that the current device runs at once; asked once a device.
+template <int DH> cudaError_t clusters(int x, int *room) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev][3];
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int have = dev < kMaxDev ? known[dev][x].load(std::memory_order_acquire) : 0;
+  if (have > 0) {
+    *room = have - 1;
+    return cudaSuccess;
+  }
+  e = opt_in_smem(attn_fwd_tc_kernel<DH, true>, Cfg<DH>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = cluster_config<DH>(attr, 2u << x, 1);
+  e = cudaOccupancyMaxActiveClusters(room, attn_fwd_tc_kernel<DH, true>, &cfg);
+  if (e == cudaSuccess && dev < kMaxDev) known[dev][x].store(*room + 1, std::memory_order_release);
+  return e;
+}
+
+template <int DH, bool kSplit> cudaError_t start(const AttnArgs &p, const Params &prm, cudaStream_t st) {
   using C = Cfg<DH>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = opt_in_smem(attn_fwd_tc_kernel<DH>, C::kSmem, done);
+  const cudaError_t e = opt_in_smem(attn_fwd_tc_kernel<DH, kSplit>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   if (!attn_map(&mq, p.q, p.B, p.T, p.Hq, DH, kBM) || !attn_map(&mk, p.k, p.B, p.S, p.Hkv, DH, kBN) ||
       !attn_map(&mv, p.v, p.B, p.S, p.Hkv, DH, kBN))
     return cudaErrorInvalidValue;
+  if constexpr (kSplit) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = cluster_config<DH>(attr, static_cast<unsigned>(prm.parts), prm.units);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, attn_fwd_tc_kernel<DH, true>, mq, mk, mv, prm);
+  }
+  attn_fwd_tc_kernel<DH, kSplit>
+      <<<prm.units < 148u ? prm.units : 148u, C::kThreads, C::kSmem, st>>>(mq, mk, mv, prm);
+  return cudaGetLastError();
+}
+
+template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
+  using C = Cfg<DH>;
   Params prm;
   prm.a = p;
   prm.rows2 = C::kNQ == 2 && (p.Hq / p.Hkv) % 2 != 0 ? 1 : 0;
@@ -673,8 +846,25 @@ template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
   prm.units = static_cast<unsigned>(static_cast<long long>(prm.n_qt) * p.B * prm.n_h);
   prm.v8 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 ? 1 : 0;
   prm.c = p.scale * kLog2e;
-  attn_fwd_tc_kernel<DH><<<prm.units < 148u ? prm.units : 148u, C::kThreads, C::kSmem, st>>>(mq, mk, mv, prm);
-  return cudaGetLastError();
+  // While units leave half of the SMs idle, a cluster of 2, 4 or 8 blocks takes each,
+  // kLeast key tiles or more a block, as long as all clusters fit on the GPU at once
+  // (16 queries, 32768 keys, 16/4 heads of 128: 472 us in one block a unit, 74 in 8).
+  // Two tiles are the least that pay: 128 queries of 16/8 heads of 128 over 512 keys
+  // take 15.3 us whole, 14.8 in two parts and 13.9 in four of one tile, but over 256
+  // keys 11.7 whole and 12.6 in two parts of one tile (256 wide 10.0 and 12.0).
+  const int last = (prm.n_qt - 1) * kBM * (1 + prm.rows2) + p.S - p.T;
+  const int most = key_tiles(last, p.S - 1, p.S, p.window, p.sinks, kBN).n;
+  prm.parts = 1;
+  for (int x = 0; x < 3; ++x) {
+    const int parts = 2 << x;
+    if (prm.units * parts > 148u || most < parts * kLeast) break;
+    int room = 0;
+    const cudaError_t e = clusters<DH>(x, &room);
+    if (e != cudaSuccess) return e;
+    if (prm.units > static_cast<unsigned>(room)) break;
+    prm.parts = parts;
+  }
+  return prm.parts > 1 ? start<DH, true>(p, prm, st) : start<DH, false>(p, prm, st);
 }
 
 }  // namespace

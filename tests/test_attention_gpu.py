@@ -194,6 +194,15 @@ ATTN_CASES = [  # io, B, T, S, Hq, Hkv, dh, window, sinks, lens, layout
     ("f32", 1, 50, 20, 2, 2, 192, 5, 1, None, "dense"),
     ("bf16", 2, 77, 77, 2, 1, 72, 20, 1, None, "slice"),
     ("f32", 1, 65, 65, 1, 1, 8, 0, 0, None, "dense"),
+    # few rows, many keys: a cluster of blocks takes a query tile's keys
+    ("bf16", 1, 128, 4096, 4, 2, 128, 0, 0, None, "dense"),
+    ("bf16", 1, 3, 2500, 3, 3, 64, 0, 0, None, "slice"),
+    ("bf16", 2, 200, 1500, 3, 1, 64, 700, 130, None, "slice"),
+    ("bf16", 1, 16, 1030, 4, 1, 256, 0, 0, None, "heads"),
+    ("bf16", 1, 1, 3000, 5, 1, 256, 2000, 0, None, "dense"),
+    ("bf16", 3, 1000, 1000, 1, 1, 64, 0, 0, [1000, 0, 300], "slice"),
+    ("bf16", 2, 640, 640, 2, 2, 128, 400, 3, [640, 129], "heads"),
+    ("bf16", 1, 600, 500, 2, 1, 128, 0, 0, None, "dense"),
 ]
 
 
@@ -281,7 +290,8 @@ def test_local_attn_bwd(cuda_device, case):
         assert all(torch.equal(got[n][b, :m], again[n][b, :m]) for n in grads for b, m in enumerate(lens))
 
 
-@pytest.mark.parametrize("io,dh,T,G", [("bf16", 64, 300, 2), ("bf16", 128, 40, 1), ("bf16", 256, 200, 2),
+@pytest.mark.parametrize("io,dh,T,G", [("bf16", 64, 300, 2), ("bf16", 64, 700, 2), ("bf16", 128, 40, 1),
+                                       ("bf16", 128, 1100, 1), ("bf16", 256, 200, 2),
                                        ("f32", 64, 90, 2), ("f32", 256, 40, 1)])
 def test_nan_reaches_who_sees_it_alone(cuda_device, io, dh, T, G):
     """A NaN in a query is that query's output; a NaN in a key that of the queries that see it."""
