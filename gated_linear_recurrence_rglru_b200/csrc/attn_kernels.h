@@ -89,7 +89,7 @@ struct PiecePlan {
 };
 
 PiecePlan attn_plan(int B, int T, int S, int Hq, int Hkv, int window, int sinks, int tile,
-                    int step, int target_blocks);
+                    int step, int target_blocks, int least);
 
 // Shared by every backward: delta[b, h, t] = sum_d dout * out (float, B * Hq * T,
 // its room rounded up), and the join of the pieces' partial sums.

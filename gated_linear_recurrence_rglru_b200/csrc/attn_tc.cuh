@@ -81,20 +81,6 @@ template <int N> __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(-N));
 }
 
-// Two or four floats of the shared memory of a block of the cluster.
-__device__ __forceinline__ void ld_cluster(uint32_t addr, float &a, float &b) {
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // N threads of the softmax warps meet.
 template <int N> __device__ __forceinline__ void bar_sync_softmax() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");

@@ -639,7 +639,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap q_rows, const __grid_cons
 // without cuts, 283 us with pieces of half, 318 us of a fifth of a tile).
 PiecePlan plan_of(const AttnArgs &p) {
   return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, kBM, p.dh == 256 ? 64 : 128,
-                   p.dh == 256 ? 43 : 64);
+                   p.dh == 256 ? 43 : 64, 4);
 }
 
 template <int DH>

@@ -27,8 +27,8 @@
 //
 // Every wait is bounded; on expiry the kernel records RGLRU_ERR_TIMEOUT (wait
 // site 7), drains what it issued and returns.
+#include "attn_cluster.cuh"
 #include "attn_tc.cuh"
-#include "tc_pair.cuh"
 
 namespace rglru {
 namespace {
@@ -189,8 +189,7 @@ template <int DH> __device__ __forceinline__ int fill_of(int i, bool is_v, int n
 
 // The parts of a split unit to its rows: every block of the cluster leaves O (not
 // divided yet), m and l of its keys in its shared memory, where the operands were, and
-// each joins its share of the rows (half of them at most) from all, in the order of the parts:
-//   M = max m_i,  f_i = 2^(m_i - M),  L = sum l_i f_i,  out = sum O_i f_i / L
+// each joins its share of the rows (half of them at most) from all.
 template <int DH, typename Un>
 __device__ __forceinline__ void join(const Params &prm, const Un &un, uint32_t t_o, bool some, int q, int g,
                                      int row, float m, float l, unsigned char *sm) {
@@ -220,24 +219,10 @@ __device__ __forceinline__ void join(const Params &prm, const Un &un, uint32_t t
   const uint32_t mine = smem_u32(part);
   if (tid < share) {                                     // f_i / L of a row
     const int x = x0 + tid, y = x / kBM, t = un.first(y) + x % kBM;
-    float pm[8], pl[8], top = -INFINITY, sum = 0.0f;
+    float f[8], top, sum;
+    join_factors<true>(mine + (kRows * kPitch + 2 * x) * 4, parts, f, top, sum);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      pm[i] = -INFINITY;
-      pl[i] = 0.0f;
-      if (i < parts) ld_cluster(mapa_shared(mine + (kRows * kPitch + 2 * x) * 4, i), pm[i], pl[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (pl[i] != 0.0f) top = fmaxf(top, pm[i]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      pm[i] = pl[i] == 0.0f ? 0.0f : ex2(pm[i] - top);
-      sum += pl[i] * pm[i];
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) fs[tid * 8 + i] = pl[i] == 0.0f ? 0.0f : pm[i] * inv;
+    for (int i = 0; i < 8; ++i) fs[tid * 8 + i] = f[i];
     if (t < un.n.nq && p.lse != nullptr)
       p.lse[(static_cast<long long>(un.b) * p.Hq + un.head(y)) * p.T + t] =
           sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
@@ -779,43 +764,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-template <int DH> cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *attr, unsigned parts, unsigned units) {
-  using C = Cfg<DH>;
-  cudaLaunchConfig_t cfg = {};
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = parts;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg.gridDim = dim3(units * parts);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
-// Clusters of 2 << x blocks that the current device runs at once; asked once a device.
-template <int DH> cudaError_t clusters(int x, int *room) {
-  constexpr int kMaxDev = 64;
-  static std::atomic<int> known[kMaxDev][3];
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const int have = dev < kMaxDev ? known[dev][x].load(std::memory_order_acquire) : 0;
-  if (have > 0) {
-    *room = have - 1;
-    return cudaSuccess;
-  }
-  e = opt_in_smem(attn_fwd_tc_kernel<DH, true>, Cfg<DH>::kSmem, done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = cluster_config<DH>(attr, 2u << x, 1);
-  e = cudaOccupancyMaxActiveClusters(room, attn_fwd_tc_kernel<DH, true>, &cfg);
-  if (e == cudaSuccess && dev < kMaxDev) known[dev][x].store(*room + 1, std::memory_order_release);
-  return e;
-}
-
 template <int DH, bool kSplit> cudaError_t start(const AttnArgs &p, const Params &prm, cudaStream_t st) {
   using C = Cfg<DH>;
   static std::atomic<unsigned long long> done{0};
@@ -826,9 +774,9 @@ template <int DH, bool kSplit> cudaError_t start(const AttnArgs &p, const Params
       !attn_map(&mv, p.v, p.B, p.S, p.Hkv, DH, kBN))
     return cudaErrorInvalidValue;
   if constexpr (kSplit) {
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = cluster_config<DH>(attr, static_cast<unsigned>(prm.parts), prm.units);
-    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    const unsigned parts = static_cast<unsigned>(prm.parts);
+    const cudaLaunchConfig_t cfg = cluster_config(&attr, parts, dim3(prm.units * parts), C::kThreads, C::kSmem, st);
     return cudaLaunchKernelEx(&cfg, attn_fwd_tc_kernel<DH, true>, mq, mk, mv, prm);
   }
   attn_fwd_tc_kernel<DH, kSplit>
@@ -854,16 +802,11 @@ template <int DH> cudaError_t launch(const AttnArgs &p, cudaStream_t st) {
   // keys 11.7 whole and 12.6 in two parts of one tile (256 wide 10.0 and 12.0).
   const int last = (prm.n_qt - 1) * kBM * (1 + prm.rows2) + p.S - p.T;
   const int most = key_tiles(last, p.S - 1, p.S, p.window, p.sinks, kBN).n;
-  prm.parts = 1;
-  for (int x = 0; x < 3; ++x) {
-    const int parts = 2 << x;
-    if (prm.units * parts > 148u || most < parts * kLeast) break;
-    int room = 0;
-    const cudaError_t e = clusters<DH>(x, &room);
-    if (e != cudaSuccess) return e;
-    if (prm.units > static_cast<unsigned>(room)) break;
-    prm.parts = parts;
-  }
+  static std::atomic<unsigned long long> done{0};
+  static ClusterRoom room;
+  const cudaError_t e = cluster_parts(attn_fwd_tc_kernel<DH, true>, C::kThreads, C::kSmem, &done, &room, prm.units,
+                                      most / kLeast, &prm.parts);
+  if (e != cudaSuccess) return e;
   return prm.parts > 1 ? start<DH, true>(p, prm, st) : start<DH, false>(p, prm, st);
 }
 

@@ -15,6 +15,7 @@
 // warp reads fall into different banks. Tiles outside the mask are skipped.
 // Hidden keys get weight zero by selection, never by arithmetic on what lies
 // there, and rows past a sequence are read as zeros.
+#include "attn_cluster.cuh"
 #include "attn_kernels.h"
 #include "attn_mask.cuh"
 #include "common.cuh"
@@ -169,13 +170,15 @@ template <int BT, int NC> constexpr int bwd_smem() {
   return (4 * BT * (NC * 64 + 4) + 2 * BT * (BT + 4) + 2 * BT) * 4;
 }
 
-template <typename T, int BT, int NC>
-__global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnArgs p) {
+// kSplit: the blocks of a cluster of `blocks` share a query tile's keys.
+template <typename T, int BT, int NC, bool kSplit>
+__global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnArgs p, const int blocks) {
   extern __shared__ __align__(16) float smf[];
   constexpr int kPitch = NC * 64 + 4, N = BT / 16, kWp = BT + 4;
   float *qs = smf, *kvs = qs + BT * kPitch, *ps = kvs + 4 * BT * kPitch;   // K and V: two buffers
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int h = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
+  const int parts = kSplit ? blocks : 1;
+  const int part = blockIdx.x % parts, row = blockIdx.x / parts, h = row % p.Hq, b = row / p.Hq;
   // the last queries first: they see the most keys
   const int q0 = (gridDim.y - 1 - blockIdx.y) * BT, off = p.S - p.T;
   const RowLens n = row_lens(p, b);
@@ -196,16 +199,17 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
   }
   // positions of the tile's queries bound which keys any of them sees
   const int seen_lo = p.window > 0 ? q0 + off - p.window + 1 : 0, seen_hi = qe + off;
+  const int x0 = kt.n * part / parts, x1 = kt.n * (part + 1) / parts;   // this block's tiles
   auto ahead = [&](int x) {
-    if (x < kt.n) {
+    if (x < x1) {
       float *d = kvs + (x & 1) * 2 * BT * kPitch;
       fill_ahead<T, BT, NC>(d, kp, p.k.st, kt.tile(x) * BT, n.nk, p.dh);
       fill_ahead<T, BT, NC>(d + BT * kPitch, vp, p.v.st, kt.tile(x) * BT, n.nk, p.dh);
     }
     fill_commit();
   };
-  ahead(0);
-  for (int x = 0; x < kt.n; ++x) {
+  ahead(x0);
+  for (int x = x0; x < x1; ++x) {
     const int k0 = kt.tile(x) * BT;
     float *ks = kvs + (x & 1) * 2 * BT * kPitch, *vs = ks + BT * kPitch;
     ahead(x + 1);
@@ -255,6 +259,46 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
     __syncthreads();                               // the buffer may be filled again
   }
   fill_wait<0>();
+  if constexpr (kSplit) {
+    // O (not divided yet), m and l to shared memory, where Q was, for the cluster's
+    // blocks; each joins its share of the rows
+    const int share = BT / parts, r0 = part * share;
+    float *ml = kvs, *fs = ml + 2 * BT;
+    if (x0 == x1) __syncthreads();                       // (Q was filled, not used)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = ty + 16 * i;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) *reinterpret_cast<float4 *>(qs + r * kPitch + tx * 4 + c * 64) = o[i][c];
+      if (tx == 0) *reinterpret_cast<float2 *>(ml + 2 * r) = make_float2(m[i], l[i]);
+    }
+    tc::cluster_sync();
+    const uint32_t o_at = tc::smem_u32(qs), ml_at = tc::smem_u32(ml);
+    for (int r = threadIdx.x; r < share; r += kThreads) {
+      const int t = q0 + r0 + r;
+      float f[8], top, sum;
+      join_factors<false>(ml_at + 2 * (r0 + r) * 4, parts, f, top, sum);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fs[r * 8 + i] = f[i];
+      if (t < n.nq && p.lse != nullptr)
+        p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] = sum == 0.0f ? -INFINITY : top + logf(sum);
+    }
+    __syncthreads();
+    for (int z = threadIdx.x; z < share * NC * 16; z += kThreads) {
+      const int r = z / (NC * 16), c = z % (NC * 16) * 4, t = q0 + r0 + r;
+      if (t >= n.nq || c >= p.dh) continue;
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const float f = fs[r * 8 + i];
+        const float4 x = ld_cluster4(tc::mapa_shared(o_at + ((r0 + r) * kPitch + c) * 4, i));
+        if (f != 0.0f) a = make_float4(fmaf(x.x, f, a.x), fmaf(x.y, f, a.y), fmaf(x.z, f, a.z), fmaf(x.w, f, a.w));
+      }
+      store4<T>(static_cast<T *>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh + c, a, 1.0f);
+    }
+    tc::cluster_sync();                                  // the others have read this block's part
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int t = q0 + ty + 16 * i;
@@ -297,15 +341,16 @@ __device__ __forceinline__ void tile_grads(const AttnArgs &p, const float *qs, c
 }
 
 // dQ: a block takes BT queries of one head and walks the keys they see.
-template <typename T, int BT, int NC>
+template <typename T, int BT, int NC, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
-attn_dq_generic_kernel(const AttnArgs p, const float *delta) {
+attn_dq_generic_kernel(const AttnArgs p, const float *delta, const int blocks) {
   extern __shared__ __align__(16) float smf[];
   constexpr int kPitch = NC * 64 + 4, N = BT / 16, kWp = BT + 4;
   float *qs = smf, *dos = qs + BT * kPitch, *ks = dos + BT * kPitch, *vs = ks + BT * kPitch;
   float *dss = vs + BT * kPitch, *lses = dss + 2 * BT * kWp, *deltas = lses + BT;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int h = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
+  const int parts = kSplit ? blocks : 1;
+  const int part = blockIdx.x % parts, row = blockIdx.x / parts, h = row % p.Hq, b = row / p.Hq;
   const int q0 = (gridDim.y - 1 - blockIdx.y) * BT, off = p.S - p.T;
   const RowLens n = row_lens(p, b);
   if (q0 >= n.nq) return;
@@ -328,7 +373,8 @@ attn_dq_generic_kernel(const AttnArgs p, const float *delta) {
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int c = 0; c < NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < kt.n; ++x) {
+  const int x1 = kt.n * (part + 1) / parts;                  // this block's tiles
+  for (int x = kt.n * part / parts; x < x1; ++x) {
     const int k0 = kt.tile(x) * BT;
     __syncthreads();
     fill<T, BT, NC>(ks, kp, p.k.st, k0, n.nk, p.dh);
@@ -350,6 +396,31 @@ attn_dq_generic_kernel(const AttnArgs p, const float *delta) {
     }
     __syncthreads();
     add_product<BT, NC, false>(o, dss, ks, tx, ty);
+  }
+  if constexpr (kSplit) {
+    // each block of the cluster adds its share of the rows up, in the order of the parts
+    const int share = BT / parts, r0 = part * share;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float4 *>(qs + (ty + 16 * i) * kPitch + tx * 4 + c * 64) = o[i][c];
+    tc::cluster_sync();
+    const uint32_t at = tc::smem_u32(qs);
+    for (int z = threadIdx.x; z < share * NC * 16; z += kThreads) {
+      const int r = z / (NC * 16), c = z % (NC * 16) * 4, t = q0 + r0 + r;
+      if (t >= n.nq || c >= p.dh) continue;
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const float4 x = ld_cluster4(tc::mapa_shared(at + ((r0 + r) * kPitch + c) * 4, i));
+        a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      }
+      store4<T>(static_cast<T *>(p.dq) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh + c, a, 1.0f);
+    }
+    tc::cluster_sync();                                  // the others have read this block's part
+    return;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -508,16 +579,40 @@ attn_join_kernel(const AttnArgs p, const PiecePlan pl, const float *__restrict__
   }
 }
 
+// Launches a kernel with a block for each query tile of BT; where those are few, its
+// split form with a cluster of blocks for each (fp32, 30 queries, 4 heads of 64: 2048
+// keys 183 us in one block, 27 in 8; 128 keys 14.0 in one, 9.9 in two, 7.2 in four of
+// one tile each).
+template <int BT, typename K, typename... Args>
+cudaError_t run_queries(K kernel, K split, int smem, const AttnArgs &p, std::atomic<unsigned long long> (&done)[2],
+                        ClusterRoom *room, cudaStream_t st, Args... args) {
+  const int tiles = ceil_div(p.T, BT), last = (tiles - 1) * BT + p.S - p.T;
+  const long long units = static_cast<long long>(p.B) * p.Hq * tiles;
+  int parts = 1;
+  cudaError_t e = cluster_parts(split, kThreads, smem, &done[1], room, static_cast<unsigned>(units < 149 ? units : 149),
+                                key_tiles(last, p.S - 1, p.S, p.window, p.sinks, BT).n, &parts);
+  if (e != cudaSuccess) return e;
+  dim3 grid(static_cast<unsigned>(p.B) * p.Hq, tiles);
+  if (parts > 1) {
+    grid.x *= parts;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_config(&attr, parts, grid, kThreads, smem, st);
+    return cudaLaunchKernelEx(&cfg, split, args..., parts);
+  }
+  e = opt_in_smem(kernel, smem, done[0]);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, st>>>(args..., 1);
+  return cudaGetLastError();
+}
+
 template <typename T, int BT, int NC>
 cudaError_t run_fwd(const AttnArgs &p, cudaStream_t st) {
   constexpr int smem = fwd_smem<BT, NC>();
   static_assert(smem <= kMaxSmem, "shared memory");
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = opt_in_smem(attn_fwd_generic_kernel<T, BT, NC>, smem, done);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.B) * p.Hq, ceil_div(p.T, BT));
-  attn_fwd_generic_kernel<T, BT, NC><<<grid, kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  static std::atomic<unsigned long long> done[2];
+  static ClusterRoom room;
+  return run_queries<BT>(attn_fwd_generic_kernel<T, BT, NC, false>, attn_fwd_generic_kernel<T, BT, NC, true>, smem, p,
+                         done, &room, st, p);
 }
 
 template <typename T, int BT, int NC>
@@ -525,14 +620,12 @@ cudaError_t run_bwd(const AttnArgs &p, const float *delta, const PiecePlan &pl, 
                     cudaStream_t st) {
   constexpr int smem = bwd_smem<BT, NC>();
   static_assert(smem <= kMaxSmem, "shared memory");
-  static std::atomic<unsigned long long> done_q{0}, done_kv{0};
-  cudaError_t e = opt_in_smem(attn_dq_generic_kernel<T, BT, NC>, smem, done_q);
+  static std::atomic<unsigned long long> done_q[2], done_kv{0};
+  static ClusterRoom room;
+  cudaError_t e = run_queries<BT>(attn_dq_generic_kernel<T, BT, NC, false>, attn_dq_generic_kernel<T, BT, NC, true>,
+                                  smem, p, done_q, &room, st, p, delta);
   if (e != cudaSuccess) return e;
   e = opt_in_smem(attn_dkv_generic_kernel<T, BT, NC>, smem, done_kv);
-  if (e != cudaSuccess) return e;
-  const dim3 gq(static_cast<unsigned>(p.B) * p.Hq, ceil_div(p.T, BT));
-  attn_dq_generic_kernel<T, BT, NC><<<gq, kThreads, smem, st>>>(p, delta);
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 gk(pl.slots, static_cast<unsigned>(p.B) * p.Hkv);
   attn_dkv_generic_kernel<T, BT, NC><<<gk, kThreads, smem, st>>>(p, delta, pl, parts);
@@ -541,9 +634,11 @@ cudaError_t run_bwd(const AttnArgs &p, const float *delta, const PiecePlan &pl, 
 
 int bwd_tile(int dh) { return dh <= 128 ? 64 : 48; }
 
+// Pieces of one step and more: a step takes longer than a partial sum (fp32, 256
+// queries, 4 heads of 64: 68 us with 4 steps or more, 48 with 2, 36 with 1).
 PiecePlan generic_plan_of(const AttnArgs &p) {
   const int bt = bwd_tile(p.dh);
-  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 148);
+  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 148, 1);
 }
 
 template <typename T> cudaError_t bwd_typed(const AttnArgs &p, void *ws, cudaStream_t st) {
@@ -584,7 +679,7 @@ template <typename T> cudaError_t fwd_typed(const AttnArgs &p, cudaStream_t st) 
 }  // namespace
 
 PiecePlan attn_plan(int B, int T, int S, int Hq, int Hkv, int window, int sinks, int tile,
-                    int step, int target_blocks) {
+                    int step, int target_blocks, int least) {
   PiecePlan pl;
   pl.tile = tile;
   pl.step = step;
@@ -603,10 +698,10 @@ PiecePlan attn_plan(int B, int T, int S, int Hq, int Hkv, int window, int sinks,
       most = n > most ? n : most;
   }
   total *= static_cast<long long>(B) * Hkv;
-  // pieces of the average block's share, never shorter than 4 steps: a piece
+  // pieces of the average block's share, never shorter than `least` steps: a piece
   // costs a partial sum of its tile, written and read again
   long long len = (total + target_blocks - 1) / target_blocks;
-  if (len < 4) len = 4;
+  if (len < least) len = least;
   pl.len = static_cast<int>(len);
   pl.pieces = most > 0 ? ceil_div(most, pl.len) : 1;
   pl.sink_pieces = most_sink > 0 ? ceil_div(most_sink, pl.len) : 1;
