@@ -97,8 +97,12 @@ __device__ __forceinline__ void dot_rows(float (&acc)[N][N], const float *a, con
   }
 }
 
-// o[i][c] += sum_k w[k][ty + 16 i] v[k][4 tx + 64 c ..]: weights stored key-major
-// (wt[k][row], pitch BT + 4) or row-major (w[row][k]).
+// The rows of a thread's part of a product whose weights are stored key-major: four
+// together where it has four, for one load.
+template <int N> __device__ __forceinline__ int part_row(int ty, int i) { return N == 4 ? ty * 4 + i : ty + 16 * i; }
+
+// o[i][c] += sum_k w[k][row i] v[k][4 tx + 64 c ..]: weights stored key-major
+// (wt[k][row], pitch BT + 4; rows of part_row) or row-major (w[row][k]; rows ty + 16 i).
 template <int BT, int NC, bool kTransposed>
 __device__ __forceinline__ void add_product(float4 (&o)[BT / 16][NC], const float *w, const float *v,
                                             int tx, int ty) {
@@ -106,9 +110,20 @@ __device__ __forceinline__ void add_product(float4 (&o)[BT / 16][NC], const floa
 #pragma unroll 2
   for (int k = 0; k < BT; k += 4) {
     float wv[N][4];
+    if constexpr (kTransposed && N == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 x = *reinterpret_cast<const float4 *>(w + (k + e) * kWp + ty * 4);
+        wv[0][e] = x.x;
+        wv[1][e] = x.y;
+        wv[2][e] = x.z;
+        wv[3][e] = x.w;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (kTransposed) {
+      if constexpr (kTransposed) {
+        if (N == 4) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e) wv[i][e] = w[(k + e) * kWp + ty + 16 * i];
       } else {
@@ -297,20 +312,20 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_generic_kernel(const AttnAr
       store4<T>(static_cast<T *>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh + c, a, 1.0f);
     }
     tc::cluster_sync();                                  // the others have read this block's part
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int t = q0 + ty + 16 * i;
-    if (t >= n.nq) continue;
-    const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-    T *dst = static_cast<T *>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh;
+    for (int i = 0; i < N; ++i) {
+      const int t = q0 + ty + 16 * i;
+      if (t >= n.nq) continue;
+      const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+      T *dst = static_cast<T *>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (tx * 4 + c * 64 < p.dh) store4<T>(dst + tx * 4 + c * 64, o[i][c], inv);
-    if (p.lse != nullptr && tx == 0)
-      p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] =
-          l[i] == 0.0f ? -INFINITY : m[i] + logf(l[i]);
+      for (int c = 0; c < NC; ++c)
+        if (tx * 4 + c * 64 < p.dh) store4<T>(dst + tx * 4 + c * 64, o[i][c], inv);
+      if (p.lse != nullptr && tx == 0)
+        p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] =
+            l[i] == 0.0f ? -INFINITY : m[i] + logf(l[i]);
+    }
   }
 }
 
@@ -420,16 +435,16 @@ attn_dq_generic_kernel(const AttnArgs p, const float *delta, const int blocks) {
       store4<T>(static_cast<T *>(p.dq) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh + c, a, 1.0f);
     }
     tc::cluster_sync();                                  // the others have read this block's part
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int t = q0 + ty + 16 * i;
-    if (t >= n.nq) continue;
-    T *dst = static_cast<T *>(p.dq) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh;
+    for (int i = 0; i < N; ++i) {
+      const int t = q0 + ty + 16 * i;
+      if (t >= n.nq) continue;
+      T *dst = static_cast<T *>(p.dq) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * p.dh;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (tx * 4 + c * 64 < p.dh) store4<T>(dst + tx * 4 + c * 64, o[i][c], 1.0f);
+      for (int c = 0; c < NC; ++c)
+        if (tx * 4 + c * 64 < p.dh) store4<T>(dst + tx * 4 + c * 64, o[i][c], 1.0f);
+    }
   }
 }
 
@@ -488,7 +503,7 @@ attn_dkv_generic_kernel(const AttnArgs p, const float *delta, const PiecePlan pl
                       2 * BT * p.dh;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int r = ty + 16 * i, j = k0 + r;
+    const int r = part_row<N>(ty, i), j = k0 + r;
     if (j >= n.nk) continue;
     const size_t dst = ((static_cast<size_t>(b) * p.S + j) * p.Hkv + kvh) * p.dh;
 #pragma unroll
@@ -635,10 +650,13 @@ cudaError_t run_bwd(const AttnArgs &p, const float *delta, const PiecePlan &pl, 
 int bwd_tile(int dh) { return dh <= 128 ? 64 : 48; }
 
 // Pieces of one step and more: a step takes longer than a partial sum (fp32, 256
-// queries, 4 heads of 64: 68 us with 4 steps or more, 48 with 2, 36 with 1).
+// queries, 4 heads of 64: 68 us with 4 steps or more, 48 with 2, 36 with 1). Four
+// pieces an SM: shorter ones even the blocks out and keep the fp32 sums short (5 x 1009,
+// 20/2 heads of 64: 2.27 ms and 7.2e-7 of dK off with one an SM, 1.70 ms and 4.9e-7
+// with four; 2 x 1024, 8/1 heads, window 256: 230 us and 156).
 PiecePlan generic_plan_of(const AttnArgs &p) {
   const int bt = bwd_tile(p.dh);
-  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 148, 1);
+  return attn_plan(p.B, p.T, p.S, p.Hq, p.Hkv, p.window, p.sinks, bt, bt, 592, 1);
 }
 
 template <typename T> cudaError_t bwd_typed(const AttnArgs &p, void *ws, cudaStream_t st) {
