@@ -8,22 +8,33 @@
 // head and the key tiles that their mask leaves, the next unit's copies and first
 // scores running while the softmax warps store the last one's rows. Heads 64 and
 // 128 wide: a block works on two query tiles at once, which share every K and V
-// tile (two heads of a group, or two tiles of one head): while the softmax
-// works on one's scores, the tensor core does the other's P V and next S.
-// 256 wide: one query tile (O takes 256 TMEM columns) with two score buffers, S of
-// the next key tile is made while the softmax works on this one.
+// tile (two heads of a group, or two tiles of one head): while the softmax works on
+// one's scores, the tensor core does the other's P V and next S. 256 wide: one query
+// tile (O takes 256 TMEM columns) with two score buffers, S of the next key tile is
+// made while the softmax works on this one. Where units would leave SMs idle, a
+// cluster of blocks shares a unit's key tiles (join).
 //
 // Eight softmax warps, thread = query row = TMEM lane: with two query tiles a thread
-// has all 128 scores of its row and key tile in registers; with one, two warp groups
-// share the columns, and a row's maximum is one exchange through shared memory
-// between two threads. One warp issues the TMA copies (K and V through one
-// ring of slots, 128 keys x up to 128 columns each, in the order of use), one the
-// MMAs: S from shared memory (Q and K both K-major), P V with P as the TMEM operand
-// (bf16, written over the scores it came from) and V MN-major as TMA left it. The
-// accumulator O stays in TMEM for a unit's whole walk; the reference maximum m moves
-// only when it is 8 or more behind in log2 units (weights up to 2^8 keep their
-// relative precision), so O is seldom rescaled. Where the mask cuts a tile, the
-// keys that a row sees are bits, and only warps that have a hidden one apply them.
+// has all 128 scores of its row and key tile in registers (16 warps with half a row
+// each: 25 % slower, for the exchange of the maximum and the spills); with one, two
+// warp groups share the columns, and a row's maximum is one exchange through shared
+// memory between two threads. One warp issues the TMA copies (K and V through one
+// ring of slots, 128 keys x up to 128 columns each, in the order of use), one or two
+// the MMAs: S from shared memory (Q and K both K-major), P V with P as the TMEM
+// operand (bf16, written over the scores it came from, or, 64 wide, to columns of its
+// own) and V MN-major as TMA left it. Weights are handed over in halves, so that P V
+// starts while the second half is formed. The accumulator O stays in TMEM for a unit's
+// whole walk; the reference maximum m moves only when it is 8 or more behind in log2
+// units (weights up to 2^8 keep their relative precision), so O is seldom rescaled.
+// Where the mask cuts a tile, the keys that a row sees are bits, and only warps that
+// have a hidden one apply them. Weights are rounded to bf16 for the product with V, as
+// its operand has to be, and summed before that.
+//
+// Bound by the way round from scores to weights and back, of which a query tile's
+// softmax is half: 8192 tokens, 16/4 heads of 128, window 2048, take 129 us (930
+// TFLOP/s, the tensor pipe half busy); 4 x 2048 tokens, 10 query heads on one 256-wide
+// key head, window 1024, 72 us (890 TFLOP/s); short windows of ragged rows (5 x 777, 16
+// heads of 64, window 256) 27 us, half of it the starts and ends of units.
 //
 // Every wait is bounded; on expiry the kernel records RGLRU_ERR_TIMEOUT (wait
 // site 7), drains what it issued and returns.
@@ -333,200 +344,200 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   // The block is launched with 168 registers a thread (12 warps); the copy and MMA
   // warps give up some of theirs to the softmax warps: 8 x 208 + 4 x 88 = 12 x 168.
   if (warp >= kTma) {
-  set_registers<-88>();
-  if (warp == kTma) {
-    // ============================ TMA producer ============================
-    if (lane == 0) {
-      int f = 0, nu[2] = {0, 0};                         // fills and query tiles issued
-      bool ok = true;
-      for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
-        const Un un(prm, u);
-        if (un.kt.n == 0) continue;
-        const int kvh = un.h / (p.Hq / p.Hkv);
-        const int fills = 2 * un.kt.n * C::kPer;
-        // K and V tiles in the order of fill_of; Q after the first of them, which
-        // may come while the last unit still uses its Q
-        int ik = 0, iv = 0;
-        for (int g = 0; g < fills && ok;) {
-          const bool is_v = !(ik < un.kt.n && fill_of<DH>(ik, false, un.kt.n) == g);
-          const int i = is_v ? iv++ : ik++;
-          for (int x = 0; x < C::kPer && ok; ++x, ++g, ++f) {
-            const int s = f % C::kSlots;
-            if (!mbar_wait(&empty[s], ((f / C::kSlots) & 1) ^ 1, abort, kWaitNs)) {
-              give_up();
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&full[s], C::kSlotBytes);
-            for (int c = 0; c < C::kCols / 64; ++c)
-              tma_load_4d(sm + C::kOffRing + s * C::kSlotBytes + c * (kBN * 128), is_v ? &tmap_v : &tmap_k,
-                          &full[s], x * C::kCols + c * 64, un.tile(i) * kBN, kvh, un.b);
-          }
-          if (ok && !is_v && i == 0) {
-            for (int q = 0; q < C::kNQ && ok; ++q) {
-              if (!mbar_wait(&q_empty[q], (nu[q] & 1) ^ 1, abort, kWaitNs)) {
+    set_registers<-88>();
+    if (warp == kTma) {
+      // ============================ TMA producer ============================
+      if (lane == 0) {
+        int f = 0, nu[2] = {0, 0};                         // fills and query tiles issued
+        bool ok = true;
+        for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
+          const Un un(prm, u);
+          if (un.kt.n == 0) continue;
+          const int kvh = un.h / (p.Hq / p.Hkv);
+          const int fills = 2 * un.kt.n * C::kPer;
+          // K and V tiles in the order of fill_of; Q after the first of them, which
+          // may come while the last unit still uses its Q
+          int ik = 0, iv = 0;
+          for (int g = 0; g < fills && ok;) {
+            const bool is_v = !(ik < un.kt.n && fill_of<DH>(ik, false, un.kt.n) == g);
+            const int i = is_v ? iv++ : ik++;
+            for (int x = 0; x < C::kPer && ok; ++x, ++g, ++f) {
+              const int s = f % C::kSlots;
+              if (!mbar_wait(&empty[s], ((f / C::kSlots) & 1) ^ 1, abort, kWaitNs)) {
                 give_up();
                 ok = false;
                 break;
               }
-              mbar_arrive_expect_tx(&q_full[q], C::kQBytes);
-              for (int c = 0; c < DH / 64; ++c)
-                tma_load_4d(sm + q * C::kQBytes + c * (kBM * 128), &tmap_q, &q_full[q], c * 64, un.first(q),
-                            un.head(q), un.b);
-              ++nu[q];
+              mbar_arrive_expect_tx(&full[s], C::kSlotBytes);
+              for (int c = 0; c < C::kCols / 64; ++c)
+                tma_load_4d(sm + C::kOffRing + s * C::kSlotBytes + c * (kBN * 128), is_v ? &tmap_v : &tmap_k,
+                            &full[s], x * C::kCols + c * 64, un.tile(i) * kBN, kvh, un.b);
             }
-          }
-        }
-      }
-      if (*abort) {
-        for (int q = 0; q < C::kNQ; ++q)
-          if (nu[q] > 0) mbar_wait_drain(&q_full[q], (nu[q] - 1) & 1, kDrainNs);
-        for (int j = f - 1; j >= 0 && j >= f - C::kSlots; --j)
-          mbar_wait_drain(&full[j % C::kSlots], (j / C::kSlots) & 1, kDrainNs);
-      }
-    }
-  } else if (warp < kMma + C::kIssuers) {
-    // ============================ MMA issuers =============================
-    // The whole warp walks, one elected lane issues. 64 wide, where the softmax
-    // takes longer than the tensor core, each query tile has a warp of its own, so
-    // that neither waits for the other's (batch of short windows: 31 -> 27 us). 128
-    // wide, one warp takes turns with the two: on their own, both would want the
-    // tensor core at once and the softmax units at once (128 -> 153 us on 8192
-    // tokens, 16 heads).
-    constexpr int kMine = C::kNQ / C::kIssuers;          // query tiles of this warp
-    constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
-    constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
-    const uint32_t base = smem_u32(sm);
-    const int first_q = warp - kMma;
-    bool ok = true;
-    int f0 = 0, units = 0;                               // fills and units before this unit
-    int js[kMine] = {}, jp[kMine] = {}, nu[kMine] = {};  // tiles scored, tiles added, units with a key
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
-        give_up();
-        ok = false;
-      }
-      if (ok) tc_fence_after();
-      return ok;
-    };
-    // a tile that this warp's query tiles do not see: its slots are the other warp's alone
-    auto pass = [&](int f) {
-      for (int x = 0; kMine == 1 && x < C::kPer; ++x) {  // (of two, one sees it)
-        const int s = (f + x) % C::kSlots;
-        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
-        if (elect_one()) mbar_arrive(&empty[s]);
-        __syncwarp();
-      }
-    };
-    // S of key tile i; `last`: Q has no later reader; `free`: nor has K, of this warp
-    auto scores = [&](const Un &un, int y, int i, bool last, bool free) {
-      const int q = first_q + y;
-      const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[y] % C::kNS;
-      const uint32_t d = tmem + C::kOffS + sb * kBN;
-      if (C::kApart && js[y] > 0 && !wait(&s_free[q], (js[y] - 1) & 1)) return;
-      for (int x = 0; x < C::kPer; ++x) {
-        const int s = (f + x) % C::kSlots;
-        if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
-        const uint32_t ad = desc_lo(base + q * C::kQBytes + x * (C::kCols / 64) * (kBM * 128), 16);
-        const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < C::kCols / 16; ++k) {
-            // a K step of 16 moves 32 bytes along the 128-byte row; 64-column
-            // blocks lie 128 rows x 128 bytes apart
-            const uint32_t o = ((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4;
-            mma_ss(d, ad + o, bd + o, id_s, k > 0 ? 1u : x > 0);
-          }
-          if (free) mma_commit(&empty[s]);
-          if (x == C::kPer - 1) {
-            mma_commit(&s_full[sb]);
-            if (last) mma_commit(&q_empty[q]);
-          }
-        }
-        __syncwarp();
-      }
-      ++js[y];
-    };
-    // O gains P V of key tile i, in the two halves in which the softmax warps hand
-    // the weights over; `first`, `done`: of the unit
-    auto values = [&](const Un &un, int y, int i, bool first, bool done, bool free) {
-      const int q = first_q + y;
-      const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[y] % C::kNS;
-      const uint32_t a = tmem + (C::kApart ? C::kOffP + q * (kBN / 2) : C::kOffS + sb * kBN);
-      if (first && nu[y] > 0 && !wait(&o_free[q], (nu[y] - 1) & 1)) return;
-      for (int x = 0; x < C::kPer; ++x)
-        if (!wait(&full[(f + x) % C::kSlots], ((f + x) / C::kSlots) & 1)) return;
-      for (int half = 0; half < 2; ++half) {
-        if (!wait(&p_full[half * C::kNQ * C::kNS + sb], (jp[y] / C::kNS) & 1)) return;
-        for (int x = 0; x < C::kPer; ++x) {
-          const int s = (f + x) % C::kSlots;
-          const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kBN / 32; ++k) {
-              // the first half of each group's columns, then the second
-              const int ks = C::kG == 2 ? (k >> 1) * 4 + half * 2 + (k & 1) : half * 4 + k;
-              mma_ts(tmem + q * DH + x * C::kCols, a + (C::kG == 2 ? (ks >> 2) * 64 + (ks & 3) * 8 : ks * 8),
-                     bd + ((ks * 16 * 128) >> 4), id_o, half + k > 0 ? 1u : !first);
-            }
-            if (half == 1) {
-              if (free) mma_commit(&empty[s]);
-              if (x == C::kPer - 1) {
-                mma_commit(&o_done[q]);
-                if (done) mma_commit(&all_done[q]);
+            if (ok && !is_v && i == 0) {
+              for (int q = 0; q < C::kNQ && ok; ++q) {
+                if (!mbar_wait(&q_empty[q], (nu[q] & 1) ^ 1, abort, kWaitNs)) {
+                  give_up();
+                  ok = false;
+                  break;
+                }
+                mbar_arrive_expect_tx(&q_full[q], C::kQBytes);
+                for (int c = 0; c < DH / 64; ++c)
+                  tma_load_4d(sm + q * C::kQBytes + c * (kBM * 128), &tmap_q, &q_full[q], c * 64, un.first(q),
+                              un.head(q), un.b);
+                ++nu[q];
               }
             }
           }
-          __syncwarp();
+        }
+        if (*abort) {
+          for (int q = 0; q < C::kNQ; ++q)
+            if (nu[q] > 0) mbar_wait_drain(&q_full[q], (nu[q] - 1) & 1, kDrainNs);
+          for (int j = f - 1; j >= 0 && j >= f - C::kSlots; --j)
+            mbar_wait_drain(&full[j % C::kSlots], (j / C::kSlots) & 1, kDrainNs);
         }
       }
-      ++jp[y];
-    };
-    for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
-      const Un un(prm, u);
-      const int n = un.kt.n;
-      if (n == 0) continue;
-      int end[kMine];                                    // the last tile that each sees
-      bool begun[kMine] = {};
-#pragma unroll
-      for (int y = 0; y < kMine; ++y) {
-        wait(&q_full[first_q + y], units & 1);
-        end[y] = un.last(p, first_q + y);
-        if (end[y] < 0 && ok) {                          // none: Q is not read
-          if (elect_one()) mbar_arrive(&q_empty[first_q + y]);
-          __syncwarp();
+    } else if (warp < kMma + C::kIssuers) {
+      // ============================ MMA issuers =============================
+      // The whole warp walks, one elected lane issues. 64 wide, where the softmax
+      // takes longer than the tensor core, each query tile has a warp of its own, so
+      // that neither waits for the other's (batch of short windows: 31 -> 27 us). 128
+      // wide, one warp takes turns with the two: on their own, both would want the
+      // tensor core at once and the softmax units at once (128 -> 153 us on 8192
+      // tokens, 16 heads).
+      constexpr int kMine = C::kNQ / C::kIssuers;          // query tiles of this warp
+      constexpr uint32_t id_s = idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t id_o = idesc_bf16_f32(kBM, C::kCols, false, true);
+      const uint32_t base = smem_u32(sm);
+      const int first_q = warp - kMma;
+      bool ok = true;
+      int f0 = 0, units = 0;                               // fills and units before this unit
+      int js[kMine] = {}, jp[kMine] = {}, nu[kMine] = {};  // tiles scored, tiles added, units with a key
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, abort, kWaitNs)) {
+          give_up();
+          ok = false;
         }
-      }
-      ++units;
-      auto next = [&](int y, int i) {
-        if (!ok || i >= n) return;
-        if (un.sees(p, first_q + y, i)) scores(un, y, i, i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
-        else pass(f0 + fill_of<DH>(i, false, n));
+        if (ok) tc_fence_after();
+        return ok;
       };
-      for (int i = -1; i < n && ok; ++i) {
+      // a tile that this warp's query tiles do not see: its slots are the other warp's alone
+      auto pass = [&](int f) {
+        for (int x = 0; kMine == 1 && x < C::kPer; ++x) {  // (of two, one sees it)
+          const int s = (f + x) % C::kSlots;
+          if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
+          if (elect_one()) mbar_arrive(&empty[s]);
+          __syncwarp();
+        }
+      };
+      // S of key tile i; `last`: Q has no later reader; `free`: nor has K, of this warp
+      auto scores = [&](const Un &un, int y, int i, bool last, bool free) {
+        const int q = first_q + y;
+        const int f = f0 + fill_of<DH>(i, false, un.kt.n), sb = q * C::kNS + js[y] % C::kNS;
+        const uint32_t d = tmem + C::kOffS + sb * kBN;
+        if (C::kApart && js[y] > 0 && !wait(&s_free[q], (js[y] - 1) & 1)) return;
+        for (int x = 0; x < C::kPer; ++x) {
+          const int s = (f + x) % C::kSlots;
+          if (!wait(&full[s], ((f + x) / C::kSlots) & 1)) return;
+          const uint32_t ad = desc_lo(base + q * C::kQBytes + x * (C::kCols / 64) * (kBM * 128), 16);
+          const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, 16);
+          if (elect_one()) {
 #pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-          if (C::kAhead) next(y, i + 1);
-          if (ok && i >= 0) {
-            if (un.sees(p, first_q + y, i)) {
-              values(un, y, i, !begun[y], i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
-              begun[y] = true;
-            } else {
-              pass(f0 + fill_of<DH>(i, true, n));
+            for (int k = 0; k < C::kCols / 16; ++k) {
+              // a K step of 16 moves 32 bytes along the 128-byte row; 64-column
+              // blocks lie 128 rows x 128 bytes apart
+              const uint32_t o = ((k & 3) * 32 + (k >> 2) * (kBN * 128)) >> 4;
+              mma_ss(d, ad + o, bd + o, id_s, k > 0 ? 1u : x > 0);
+            }
+            if (free) mma_commit(&empty[s]);
+            if (x == C::kPer - 1) {
+              mma_commit(&s_full[sb]);
+              if (last) mma_commit(&q_empty[q]);
             }
           }
-          if (!C::kAhead) next(y, i + 1);
+          __syncwarp();
         }
-      }
+        ++js[y];
+      };
+      // O gains P V of key tile i, in the two halves in which the softmax warps hand
+      // the weights over; `first`, `done`: of the unit
+      auto values = [&](const Un &un, int y, int i, bool first, bool done, bool free) {
+        const int q = first_q + y;
+        const int f = f0 + fill_of<DH>(i, true, un.kt.n), sb = q * C::kNS + jp[y] % C::kNS;
+        const uint32_t a = tmem + (C::kApart ? C::kOffP + q * (kBN / 2) : C::kOffS + sb * kBN);
+        if (first && nu[y] > 0 && !wait(&o_free[q], (nu[y] - 1) & 1)) return;
+        for (int x = 0; x < C::kPer; ++x)
+          if (!wait(&full[(f + x) % C::kSlots], ((f + x) / C::kSlots) & 1)) return;
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(&p_full[half * C::kNQ * C::kNS + sb], (jp[y] / C::kNS) & 1)) return;
+          for (int x = 0; x < C::kPer; ++x) {
+            const int s = (f + x) % C::kSlots;
+            const uint32_t bd = desc_lo(base + C::kOffRing + s * C::kSlotBytes, kBN * 128);
+            if (elect_one()) {
 #pragma unroll
-      for (int y = 0; y < kMine; ++y) nu[y] += begun[y] ? 1 : 0;
-      f0 += 2 * n * C::kPer;
+              for (int k = 0; k < kBN / 32; ++k) {
+                // the first half of each group's columns, then the second
+                const int ks = C::kG == 2 ? (k >> 1) * 4 + half * 2 + (k & 1) : half * 4 + k;
+                mma_ts(tmem + q * DH + x * C::kCols, a + (C::kG == 2 ? (ks >> 2) * 64 + (ks & 3) * 8 : ks * 8),
+                       bd + ((ks * 16 * 128) >> 4), id_o, half + k > 0 ? 1u : !first);
+              }
+              if (half == 1) {
+                if (free) mma_commit(&empty[s]);
+                if (x == C::kPer - 1) {
+                  mma_commit(&o_done[q]);
+                  if (done) mma_commit(&all_done[q]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+        }
+        ++jp[y];
+      };
+      for (unsigned r = 0, u; (u = unit_at<kSplit>(prm, r)) < prm.units && ok; ++r) {
+        const Un un(prm, u);
+        const int n = un.kt.n;
+        if (n == 0) continue;
+        int end[kMine];                                    // the last tile that each sees
+        bool begun[kMine] = {};
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) {
+          wait(&q_full[first_q + y], units & 1);
+          end[y] = un.last(p, first_q + y);
+          if (end[y] < 0 && ok) {                          // none: Q is not read
+            if (elect_one()) mbar_arrive(&q_empty[first_q + y]);
+            __syncwarp();
+          }
+        }
+        ++units;
+        auto next = [&](int y, int i) {
+          if (!ok || i >= n) return;
+          if (un.sees(p, first_q + y, i)) scores(un, y, i, i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
+          else pass(f0 + fill_of<DH>(i, false, n));
+        };
+        for (int i = -1; i < n && ok; ++i) {
+#pragma unroll
+          for (int y = 0; y < kMine; ++y) {
+            if (C::kAhead) next(y, i + 1);
+            if (ok && i >= 0) {
+              if (un.sees(p, first_q + y, i)) {
+                values(un, y, i, !begun[y], i == end[y], y == kMine - 1 || !un.sees(p, kMine - 1, i));
+                begun[y] = true;
+              } else {
+                pass(f0 + fill_of<DH>(i, true, n));
+              }
+            }
+            if (!C::kAhead) next(y, i + 1);
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) nu[y] += begun[y] ? 1 : 0;
+        f0 += 2 * n * C::kPer;
+      }
+      if (*abort) {                                        // let what was issued finish
+        if (elect_one()) mma_commit(drained);
+        mbar_wait_drain(drained, 0, kDrainNs);
+      }
     }
-    if (*abort) {                                        // let what was issued finish
-      if (elect_one()) mma_commit(drained);
-      mbar_wait_drain(drained, 0, kDrainNs);
-    }
-  }
   } else {
     set_registers<208>();
     // =============================== softmax ==============================
@@ -699,7 +710,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         ++j;
       }
       if constexpr (kSplit) {
-        if (begun) wait(&all_done[q], 0);
+        // (a Q that no product reads has to have landed too: join writes over it)
+        if (un.kt.n > 0) wait(begun ? &all_done[q] : &q_full[q], 0);
         if (C::kG == 2) l += exchange(l, j & 1);
         join<DH>(prm, un, t_o, ok && begun, q, g, row, m, l, sm);
         break;
