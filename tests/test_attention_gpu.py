@@ -311,6 +311,22 @@ def test_nan_reaches_who_sees_it_alone(cuda_device, io, dh, T, G):
     assert torch.isnan(got[:, 20:, 0]).all() and torch.isnan(glse[:, 0, 20:]).all()
 
 
+@pytest.mark.parametrize("io,dh,T,S,window,sinks", [("bf16", 64, 16, 16, 0, 0), ("bf16", 256, 4, 7, 0, 0),
+                                                    ("bf16", 128, 40, 40, 9, 7), ("bf16", 72, 30, 30, 16, 0),
+                                                    ("f32", 64, 10, 5, 0, 0)])
+def test_rounding_of_out_stays_out_of_rows_with_few_keys(cuda_device, io, dh, T, S, window, sinks):
+    """Queries that see up to 16 keys get their gradients from the keys: another rounding of out
+    changes no bit."""
+    gen = torch.Generator().manual_seed(71)
+    q, k, v, dout = (randn(gen, (2, n, h, dh), io).to(cuda_device) for n, h in ((T, 4), (S, 2), (S, 2), (T, 4)))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v, window=window, sinks=sinks)
+    g = rg.rglru_local_attn_bwd(q, k, v, out, lse, dout, window=window, sinks=sinks)
+    other = out * (1 + 2 * torch.finfo(out.dtype).eps)
+    assert not torch.equal(out, other)
+    again = rg.rglru_local_attn_bwd(q, k, v, other, lse, dout, window=window, sinks=sinks)
+    assert all(torch.equal(g[n], again[n]) for n in g)
+
+
 # ---------------------------------------------------------------- one token over a cache
 
 DECODE_CASES = [  # io, Hq, Hkv, dh, page, lens, window, sinks, max_pages
