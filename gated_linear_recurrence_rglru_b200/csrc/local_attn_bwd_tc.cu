@@ -72,8 +72,8 @@ template <int DH, bool kFirst, bool kSecond> struct Cfg {
   // products, it made S bound by shared memory's bandwidth (6 KB in 32 cycles), and
   // its 64 KB there are a third U and a second W buffer now.
   static constexpr bool kXT = DH == 256;
-  static constexpr int kNS = kFirst ? 1 : 2;               // score buffers
-  static constexpr int kNU = kXT ? 3 : 2, kNW = kXT && !kFirst ? 3 : 2;
+  static constexpr int kNS = kFirst && DH != 64 ? 1 : 2;   // score buffers
+  static constexpr int kNU = 3, kNW = kXT && !kFirst ? 3 : 2;
   static constexpr int kXBytes = kBM * DH * 2;
   static constexpr int kTile = kBN * DH * 2;
   static constexpr int kOffY = kXT ? 0 : kXBytes;
@@ -348,10 +348,12 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         if (wait(&p_full[i & 1], (i >> 1) & 1)) issue_second(i);
         continue;
       }
-      // P is in place, or S was read: the score columns are free after `second`
-      if (!wait(&p_full[0], i & 1)) break;
+      // P is in place, or S was read: the score columns are free after `second`, or,
+      // with two buffers, after the last tile's
+      if (C::kNS == 2 && i + 1 < wk.n) issue_s(i + 1);
+      if (!wait(&p_full[i % C::kNS], (i / C::kNS) & 1)) break;
       if (kSecond) issue_second(i);
-      if (ok && i + 1 < wk.n) issue_s(i + 1);
+      if (C::kNS == 1 && ok && i + 1 < wk.n) issue_s(i + 1);
       if (wait(ds_full, i & 1)) {
         if (elect_one()) {
           product(tmem, tmem + C::kTdP, u_at(i), i > 0);
@@ -444,7 +446,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
         if (kFirst && !kSecond) {                          // the scores may be overwritten
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[0]);
+          if (lane == 0) mbar_arrive(&p_full[sb]);
         }
         const unsigned long long cc = pair(prm.c, prm.c), mm = pair(-row_lse, -row_lse);
 #pragma unroll
