@@ -521,93 +521,118 @@ attn_dkv_generic_kernel(const AttnArgs p, const float *delta, const PiecePlan pl
   }
 }
 
-// 8 elements of a row.
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 elements of a row, as loaded.
+template <typename T> struct Row8 {
+  uint4 w[sizeof(T) / 2] = {};
+  __device__ void load(const T *p) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
   }
+  __device__ float dot(const Row8 &o, float s) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, c[4] = {o.w[i].x, o.w[i].y, o.w[i].z, o.w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          s = fmaf(__uint_as_float(a[k]), __uint_as_float(c[k]), s);
+        } else {
+          s = fmaf(__uint_as_float(a[k] << 16), __uint_as_float(c[k] << 16), s);
+          s = fmaf(__uint_as_float(a[k] & 0xFFFF0000u), __uint_as_float(c[k] & 0xFFFF0000u), s);
+        }
+      }
+    }
+    return s;
+  }
+};
+
+// delta[b, h, t] = sum_d dout * out of row (b, t, h). A query that sees few keys gets it
+// from them instead, as sum_j p_j (dout . v_j): the stored out is rounded, and that
+// error is in each of the row's score gradients alike, where it adds up while their own
+// roundings average; its share falls with the number of keys (bf16, rows of 4 tokens,
+// 10 heads of 256: dQ and dK off by 3.2e-3 with out's, 2.4e-3 so; rows of 74 tokens
+// 2.6e-3 and 2.4e-3). Those are the queries at the first kFew positions, or all where
+// window and sinks come to no more. They are a warp each, in the first blocks, so that
+// their walks over the keys run beside the others (3 us more on 4 x 2048 tokens, 10
+// heads of 256); the others are 8 lanes each.
+constexpr int kFew = 16;
+
+// The first tokens of a row whose queries see few keys.
+int few_tokens(const AttnArgs &p) {
+  if (p.window > 0 && static_cast<long long>(p.window) + p.sinks <= kFew) return p.T;
+  const long long n = kFew - (static_cast<long long>(p.S) - p.T);
+  return static_cast<int>(n < 0 ? 0 : n < p.T ? n : p.T);
 }
 
-// delta[b, h, t] = sum_d dout * out of row (b, t, h): 8 lanes a row. A query that sees
-// kFew keys or fewer gets it from them instead, as sum_j p_j (dout . v_j): the stored
-// out is rounded, and that error is in each of the row's score gradients alike, where
-// it adds up while their own roundings average; its share falls with the number of keys
-// (bf16, rows of 4 tokens, 10 heads of 256: dQ and dK off by 3.2e-3 with out's, 2.4e-3
-// so; rows of 74 tokens 2.6e-3 and 2.4e-3; for 3 us more on 4 x 2048 tokens).
-constexpr int kFew = 16, kBatch = 4;
-
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_delta_kernel(const AttnArgs p, float *delta) {
-  const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
-  const int lane = threadIdx.x & 7;
-  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / 8) + (threadIdx.x >> 3);
-  if (item >= rows) return;                         // whole groups of 8 lanes
-  // tokens slowest: the rows of few keys, which take longest, come first
+__global__ void __launch_bounds__(kThreads, 4)
+attn_delta_kernel(const AttnArgs p, float *delta, const int few, const unsigned few_blocks) {
+  const bool walk = blockIdx.x < few_blocks;
+  const int lanes = walk ? 32 : 8, lane = threadIdx.x & (lanes - 1);
+  const long long heads = static_cast<long long>(p.B) * p.Hq, rows = (walk ? few : p.T) * heads;
+  // tokens slowest
+  const long long item = walk ? static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)
+                              : few * heads + static_cast<long long>(blockIdx.x - few_blocks) * (kThreads / 8) +
+                                    (threadIdx.x >> 3);
+  if (item >= rows) return;                         // whole groups of lanes
   const int h = static_cast<int>(item % p.Hq);
   const long long tb = item / p.Hq;
   const int b = static_cast<int>(tb % p.B), t = static_cast<int>(tb / p.B);
   const long long row = (static_cast<long long>(b) * p.T + t) * p.Hq + h;
-  const unsigned mask = 0xFFu << (threadIdx.x & 24);
-  auto total = [&](float v) {                       // of the row's lanes
-#pragma unroll
-    for (int x = 4; x > 0; x >>= 1) v += __shfl_xor_sync(mask, v, x);
-    return v;
-  };
   const long long at = (static_cast<long long>(b) * p.Hq + h) * p.T + t;
+  const T *x = static_cast<const T *>(p.dout) + row * p.dh;
   const RowLens n = row_lens(p, b);
   float s = 0.0f;
-  if (t < n.nq) {
-    const T *x = static_cast<const T *>(p.dout) + row * p.dh, *y = static_cast<const T *>(p.out) + row * p.dh;
+  if (walk) {
     // the keys first .. last, and those before first that are sinks
-    const int pos = t + p.S - p.T, last = min(pos, n.nk - 1);
+    const int pos = t + p.S - p.T, last = t < n.nq ? min(pos, n.nk - 1) : -1;
     const int first = p.window > 0 ? max(pos - p.window + 1, 0) : 0, head = min(p.sinks, first);
-    const int keys = head + max(last - first + 1, 0);
-    if (last >= 0 && keys <= kFew) {
-      const int kvh = h / (p.Hq / p.Hkv);
-      const T *q = head_of<T>(p.q, b, h) + t * p.q.st, *k = head_of<T>(p.k, b, kvh), *v = head_of<T>(p.v, b, kvh);
-      const float lse = p.lse[at];
-      for (int i0 = 0; i0 < keys; i0 += kBatch) {        // kBatch keys' loads in flight
-        float qk[kBatch] = {}, dv[kBatch] = {};
-        for (int d = lane * 8; d < p.dh; d += 64) {
-          float c[8], g[8], e[8];
-          load8(q + d, c);
-          load8(x + d, g);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int z = min(i0 + i, keys - 1), j = z < head ? z : first + z - head;
-            load8(k + j * p.k.st + d, e);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) qk[i] = fmaf(c[y], e[y], qk[i]);
-            load8(v + j * p.v.st + d, e);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) dv[i] = fmaf(g[y], e[y], dv[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const float w = expf(total(qk[i]) * p.scale - lse), u = total(dv[i]);
-          if (i0 + i < keys) s = fmaf(w, u, s);
-        }
-      }
-    } else {
-      for (int d = lane * 8; d < p.dh; d += 64) {
-        float c[8], e[8];
-        load8(x + d, c);
-        load8(y + d, e);
-#pragma unroll
-        for (int z = 0; z < 8; ++z) s = fmaf(c[z], e[z], s);
-      }
-      s = total(s);
+    const int keys = last < 0 ? 0 : head + max(last - first + 1, 0);
+    // a key to 8, 16 or 32 lanes of 8 dims each (dh is 256 at most), and four such at once
+    const int wide = p.dh <= 64 ? 8 : p.dh <= 128 ? 16 : 32, slot = lane / wide, d = (lane & (wide - 1)) * 8;
+    const int kvh = h / (p.Hq / p.Hkv), at_once = 32 / wide;
+    const T *q = head_of<T>(p.q, b, h) + t * p.q.st, *k = head_of<T>(p.k, b, kvh), *v = head_of<T>(p.v, b, kvh);
+    const bool in = d < p.dh && keys > 0;
+    const float lse = keys > 0 ? p.lse[at] : 0.0f;
+    Row8<T> qs, xs;
+    if (in) {
+      qs.load(q + d);
+      xs.load(x + d);
     }
+    for (int i0 = slot; i0 < keys + slot; i0 += 4 * at_once) {             // (uniform in the warp)
+      Row8<T> ks[4], vs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int z = min(i0 + i * at_once, keys - 1), j = z < head ? z : first + z - head;
+        if (in) {
+          ks[i].load(k + j * p.k.st + d);
+          vs[i].load(v + j * p.v.st + d);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float qk = qs.dot(ks[i], 0.0f), dv = xs.dot(vs[i], 0.0f);
+        for (int w = wide / 2; w > 0; w >>= 1) {
+          qk += __shfl_xor_sync(0xFFFFFFFFu, qk, w);
+          dv += __shfl_xor_sync(0xFFFFFFFFu, dv, w);
+        }
+        if (i0 + i * at_once < keys) s = fmaf(expf(qk * p.scale - lse), dv, s);
+      }
+    }
+    for (int w = wide; w < 32; w <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
+  } else {
+    if (t < n.nq) {
+      const T *y = static_cast<const T *>(p.out) + row * p.dh;
+      for (int d = lane * 8; d < p.dh; d += 64) {
+        Row8<T> c, e;
+        c.load(x + d);
+        e.load(y + d);
+        s = c.dot(e, s);
+      }
+    }
+    const unsigned mask = 0xFFu << (threadIdx.x & 24);
+#pragma unroll
+    for (int w = 4; w > 0; w >>= 1) s += __shfl_xor_sync(mask, s, w);
   }
   if (lane == 0) delta[at] = s;
 }
@@ -789,12 +814,15 @@ size_t attn_parts_bytes(const AttnArgs &p, const PiecePlan &pl) {
 }
 
 cudaError_t launch_attn_delta(const AttnArgs &p, int io, float *delta, cudaStream_t st) {
-  const long long rows = static_cast<long long>(p.B) * p.T * p.Hq;
-  const unsigned blocks = static_cast<unsigned>((rows + kThreads / 8 - 1) / (kThreads / 8));
+  const long long heads = static_cast<long long>(p.B) * p.Hq;
+  const int few = few_tokens(p);
+  const unsigned few_blocks = static_cast<unsigned>((few * heads + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned blocks =
+      few_blocks + static_cast<unsigned>(((p.T - few) * heads + kThreads / 8 - 1) / (kThreads / 8));
   if (io == RGLRU_IO_F32)
-    attn_delta_kernel<float><<<blocks, kThreads, 0, st>>>(p, delta);
+    attn_delta_kernel<float><<<blocks, kThreads, 0, st>>>(p, delta, few, few_blocks);
   else
-    attn_delta_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(p, delta);
+    attn_delta_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(p, delta, few, few_blocks);
   return cudaGetLastError();
 }
 
