@@ -30,9 +30,12 @@
 // times the error of fp32 products that are stored in bf16). Sums are fp32.
 //
 // Bound by the tensor core and the hand-overs between it and the weight warps: 4 x 2048
-// tokens, 10 query heads on one 256-wide key head, window 1024, take 258 us (624
-// TFLOP/s of the five products that the gradients need, 1.0 PFLOP/s of the eight done);
-// 2 x 4096 tokens, 16/4 heads of 128, 390 us (880; 1.23 PFLOP/s of the seven done).
+// tokens, 10 query heads on one 256-wide key head, window 1024, take 265 us with the row
+// sums' 22 (608 TFLOP/s of the five products that the gradients need, 0.97 PFLOP/s of
+// the eight done); 2 x 4096 tokens, 16/4 heads of 128, 395 us (870; 1.22 PFLOP/s of the
+// seven done). Short walks (3 x 1535 ragged tokens, 16 heads of 64, window 512: 68 us of
+// 1152 blocks) spend 2300 cycles before the first scores, 2500 a step, of which the
+// exponentials are half, and 2600 after the last.
 //
 // All kinds of a call are one grid, the key-row blocks first. Key rows' steps
 // are cut into pieces (PiecePlan), joined by attn_join_kernel.
