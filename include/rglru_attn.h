@@ -122,7 +122,9 @@ int rglru_local_attn_fwd(const void *q, const rglru_strides *q_strides, const vo
 
 /*
  * Backward of rglru_local_attn_fwd, from its inputs, its out and lse and
- * dout = dL/dout (B, T, Hq, dh; dense), with lse constant:
+ * dout = dL/dout (B, T, Hq, dh; dense), with lse constant. (Row sums of dout and out
+ * come from out, but for queries that see few keys, 16 at most, from those: the
+ * rounding of out would tell there.)
  *   dq (B, T, Hq, dh), dk, dv (B, S, Hkv, dh)  io, dense (written; with lens,
  *   rows past a sequence are left as they were).
  * Key heads shared by several query heads get the sum of their gradients, taken
