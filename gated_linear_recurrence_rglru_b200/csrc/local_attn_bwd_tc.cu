@@ -462,7 +462,10 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           }
           unpair(fma2(pair(v[c], v[c + 1]), cc, m0), v[c], v[c + 1]);
           unpair(fma2(pair(v[c + 2], v[c + 3]), cc, m1), v[c + 2], v[c + 3]);
-          if (c % 8 == 0) {                                // a quarter of them on the FMA pipes
+          // an eighth of them on the FMA pipes (2 x 4096 tokens, 16/4 heads of 128: 395 us
+          // with none, 392 with an eighth, 391 to 394 with more; 64 wide 92 with none and
+          // an eighth, 95 and more with a quarter)
+          if (c % 16 == 0) {
             ex2_pair(v[c], v[c + 1]);
           } else {
             v[c] = ex2(v[c]);

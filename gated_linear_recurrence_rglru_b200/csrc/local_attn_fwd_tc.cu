@@ -31,7 +31,7 @@
 // its operand has to be, and summed before that.
 //
 // Bound by the way round from scores to weights and back, of which a query tile's
-// softmax is half: 8192 tokens, 16/4 heads of 128, window 2048, take 129 us (930
+// softmax is half: 8192 tokens, 16/4 heads of 128, window 2048, take 128 us (940
 // TFLOP/s, the tensor pipe half busy); 4 x 2048 tokens, 10 query heads on one 256-wide
 // key head, window 1024, 72 us (890 TFLOP/s); short windows of ragged rows (5 x 777, 16
 // heads of 64, window 256) 27 us, half of it the starts and ends of units.
@@ -65,7 +65,7 @@ template <int DH> struct Cfg {
   static constexpr int kSlotBytes = kBN * kCols * 2;
   static constexpr int kSlots = DH == 64 ? 8 : 5;
   static constexpr int kQBytes = kBM * DH * 2;           // of one query tile
-  static constexpr int kPoly = 4;                         // of 16 pairs of scores (weights32)
+  static constexpr int kPoly = 2;                        // of 16 pairs of scores (weights32)
   static constexpr int kG = kNQ == 2 ? 1 : 2;            // warp groups that share a tile's columns
   static constexpr int kSoftmax = 8;                     // softmax warps
   static constexpr int kThreads = (kSoftmax + 4) * 32;   // whole warp groups, for the register split
@@ -95,7 +95,8 @@ template <int N> __device__ __forceinline__ float max_of(const float (&v)[N][32]
 // 32 scores of a row to weights 2^(v c - m), packed as bf16; sum gains them. kPoly
 // of the 16 pairs go by ex2_pair: the hardware's 2^x gives 16 results a cycle and
 // SM, as long for a tile of 128 x 128 scores as the tensor core needs for a 128-wide
-// head, while the FMA pipes have room.
+// head, while the FMA pipes have room (8192 tokens, 16/4 heads of 128: 131 us with none
+// of them, 128 with 2, 129 with 4, 136 with 8).
 template <int kPoly>
 __device__ __forceinline__ void weights32(const float (&v)[32], unsigned long long cc,
                                           unsigned long long mm, unsigned long long (&sum)[2],
