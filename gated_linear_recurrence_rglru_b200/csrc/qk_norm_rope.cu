@@ -226,7 +226,9 @@ __device__ __forceinline__ void grad_rows(const T *src, long long sh, const T *d
       float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * inv + eps);
+      const float root = rsqrtf(row_sum<LPR>(ss) * inv + eps);
+      // (no row here: without eps its root is infinite, and 0 times that would be NaN in dw)
+      const float r = hh < h1 ? root : 0.0f;
       rotate(g, turn);
       float gx = 0.0f;
 #pragma unroll

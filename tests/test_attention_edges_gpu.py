@@ -1,0 +1,46 @@
+"""GPU tests of the local attention operators where they are easily wrong: numbers that are not
+finite, rows that see nothing, sizes at the ends of what is accepted, and calls large enough for
+every block to take several units of work. The bars are those of test_attention_gpu.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_linear_recurrence_rglru_b200 as rg
+import test_attention_gpu as base
+from oracle import attention_oracle as orc
+from test_attention_gpu import DT, U, UB, close, f64, randn
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- norms and rotation
+
+def check_norm_grads(got, x, dy, w, pos, rot, io, eps, n):
+    """dx and dw of one of q and k, within the bars of test_qk_norm_rope_bwd."""
+    x, dy, w = f64(x), f64(dy), f64(w) if w is not None else None
+    dx, dw = orc.qk_norm_rope_bwd(x, w, dy, pos.numpy(), rot, 10000.0, eps)
+    g = np.abs(dy)
+    g = g + np.concatenate([g[..., rot // 2:rot], g[..., :rot // 2], 0 * g[..., rot:]], -1)
+    r = 1 / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps)
+    xh, gw = np.abs(x * r), g * np.abs(1 if w is None else w)
+    close(got["d" + n], dx, 64 * U * r * (gw + xh * np.mean(gw * xh, -1, keepdims=True))
+          + (UB * np.abs(dx) if io == "bf16" else 0), "d" + n)
+    rows = x.shape[0] * x.shape[1] * x.shape[2]
+    close(got["dw_" + n], dw, (64 + rows) * U * (g * xh).sum((0, 1, 2)), "dw_" + n)
+
+
+@pytest.mark.parametrize("io,B,T,Hq,Hkv,dh", [("bf16", 2, 9, 10, 1, 64), ("f32", 2, 9, 3, 1, 128),
+                                              ("f32", 1, 5, 1, 1, 8), ("bf16", 3, 700, 5, 5, 40)])
+def test_norm_without_eps(cuda_device, io, B, T, Hq, Hkv, dh):
+    """eps = 0 is allowed: the places of a warp that have no row (heads that do not fill its rows)
+    add nothing to dw, not 0 times the infinite root of nothing."""
+    gen, q, k, w, pos = base.qk_inputs(io, B, T, Hq, Hkv, dh, 0, True, 81)
+    q[0, 0, 0] = randn(gen, (dh,), io)                  # (a row of zeros has no norm without eps)
+    dq, dk = randn(gen, q.shape, io), randn(gen, k.shape, io)
+    rot = dh // 16 * 16
+    d = [x.to(cuda_device) for x in (q, k, dq, dk, *w, pos)]
+    got = rg.rglru_qk_norm_rope_bwd(*d, rot=rot, eps=0.0)
+    for x, dy, wx, n in ((q, dq, w[0], "q"), (k, dk, w[1], "k")):
+        check_norm_grads(got, x, dy, wx, pos, rot, io, 0.0, n)
+        assert all(torch.isfinite(got[m]).all() for m in ("d" + n, "dw_" + n))
