@@ -179,13 +179,13 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// The largest; NaN if any is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+__device__ __forceinline__ float max2(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
@@ -194,11 +194,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
 // 2^a, 2^b for a, b <= 127 on the FMA pipes: 2^x = 2^n 2^f with n the nearest whole
 // number (read off the low bits of x + 1.5 * 2^23) and f in [-1/2, 1/2], 2^f by the
 // polynomial of degree 4 of least relative error there (2.6e-6, by Remez exchange),
-// n added to the exponent. Below -126 the result is 2^-126 to a factor of sqrt 2; for
-// NaN it is NaN or over 3e38.
-__device__ __forceinline__ void ex2_pair(float &a, float &b) {
+// times 2^n. Below -126 the result is 2^-126 to a factor of sqrt 2. For NaN it is NaN with
+// kNaN; without, where n is added to the exponent's bits instead of one product more, it
+// is the largest finite number, and the caller has to see to the NaN.
+template <bool kNaN> __device__ __forceinline__ void ex2_pair(float &a, float &b) {
   constexpr float kMagic = 12582912.0f;
-  const unsigned long long x = pair(max_nan(a, -126.0f), max_nan(b, -126.0f));
+  const unsigned long long x = pair(max2(a, -126.0f), max2(b, -126.0f));
   const unsigned long long z = add2(x, pair(kMagic, kMagic));
   const unsigned long long n = add2(z, pair(-kMagic, -kMagic));
   const unsigned long long f = fma2(n, pair(-1.0f, -1.0f), x);
@@ -206,11 +207,17 @@ __device__ __forceinline__ void ex2_pair(float &a, float &b) {
   r = fma2(r, f, pair(2.402474483e-01f, 2.402474483e-01f));
   r = fma2(r, f, pair(6.931218147e-01f, 6.931218147e-01f));
   r = fma2(r, f, pair(9.999992614e-01f, 9.999992614e-01f));
-  float za, zb, ra, rb;
+  float za, zb;
   unpair(z, za, zb);
-  unpair(r, ra, rb);
-  a = __int_as_float(__float_as_int(ra) + (__float_as_int(za) << 23));
-  b = __int_as_float(__float_as_int(rb) + (__float_as_int(zb) << 23));
+  const int na = __float_as_int(za) << 23, nb = __float_as_int(zb) << 23;
+  if constexpr (kNaN) {
+    constexpr int kOne = 0x3F800000;
+    unpair(mul2(r, pair(__int_as_float(na + kOne), __int_as_float(nb + kOne))), a, b);
+  } else {
+    unpair(r, a, b);
+    a = __int_as_float(__float_as_int(a) + na);
+    b = __int_as_float(__float_as_int(b) + nb);
+  }
 }
 
 // N floats as bf16 (2 N bytes) at dst; v8: dst is 32-byte aligned.

@@ -466,7 +466,7 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           // with none, 392 with an eighth, 391 to 394 with more; 64 wide 92 with none and
           // an eighth, 95 and more with a quarter)
           if (c % 16 == 0) {
-            ex2_pair(v[c], v[c + 1]);
+            ex2_pair<true>(v[c], v[c + 1]);
           } else {
             v[c] = ex2(v[c]);
             v[c + 1] = ex2(v[c + 1]);

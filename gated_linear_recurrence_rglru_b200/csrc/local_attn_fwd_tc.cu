@@ -80,23 +80,25 @@ template <int DH> struct Cfg {
   static_assert(kSmem <= kMaxSmem && kOffP + (kApart ? kNQ * kBN / 2 : 0) <= 512, "shared memory, TMEM");
 };
 
-// The largest of N x 32 scores, in four chains.
+// The largest of N x 32 scores, in four chains; NaN if any is.
 template <int N> __device__ __forceinline__ float max_of(const float (&v)[N][32]) {
   float m[4];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) m[x] = fmaxf(v[0][2 * x], v[0][2 * x + 1]);
+  for (int x = 0; x < 4; ++x) m[x] = max2(v[0][2 * x], v[0][2 * x + 1]);
 #pragma unroll
   for (int c = 0; c < N; ++c)
 #pragma unroll
     for (int e = c == 0 ? 8 : 0; e < 32; e += 2) m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], v[c][e], v[c][e + 1]);
-  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+  return max2(max3(m[0], m[1], m[2]), m[3]);
 }
 
 // 32 scores of a row to weights 2^(v c - m), packed as bf16; sum gains them. kPoly
 // of the 16 pairs go by ex2_pair: the hardware's 2^x gives 16 results a cycle and
 // SM, as long for a tile of 128 x 128 scores as the tensor core needs for a 128-wide
 // head, while the FMA pipes have room (8192 tokens, 16/4 heads of 128: 131 us with none
-// of them, 128 with 2, 129 with 4, 136 with 8).
+// of them, 128 with 2, 129 with 4, 136 with 8; with 2 that keep a NaN, 131). A NaN among
+// the scores makes m NaN (softmax warps), so that the hardware's results, and with them
+// the row's sum and product, are NaN.
 template <int kPoly>
 __device__ __forceinline__ void weights32(const float (&v)[32], unsigned long long cc,
                                           unsigned long long mm, unsigned long long (&sum)[2],
@@ -106,7 +108,7 @@ __device__ __forceinline__ void weights32(const float (&v)[32], unsigned long lo
     float a, b;
     unpair(fma2(pair(v[2 * e], v[2 * e + 1]), cc, mm), a, b);
     if ((e * kPoly) % 16 < kPoly) {                       // spread evenly
-      ex2_pair(a, b);
+      ex2_pair<false>(a, b);
     } else {
       a = ex2(a);
       b = ex2(b);
@@ -622,18 +624,18 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               tmem_ld32(ts + c, w[0]);
               tmem_wait_ld32(w[0]);
               hide(w[0], bits, -INFINITY);
-              top = fmaxf(top, max_of(w));
+              top = max2(top, max_of(w));
             }
           }
         }
-        if constexpr (C::kG == 2) top = fmaxf(top, exchange(top, j & 1));
+        if constexpr (C::kG == 2) top = max2(top, exchange(top, j & 1));
         if (!ok) {
           ++j;
           continue;
         }
         top *= prm.c;
-        const bool grow = top > m + kSlack || m == -INFINITY;
-        const float mn = grow ? fmaxf(top, m) : m;
+        // (a NaN moves m too, and stays in it)
+        const float mn = top <= m + kSlack ? m : max2(top, m);
         if (__any_sync(0xFFFFFFFFu, mn != m)) {
           const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
           l *= f;

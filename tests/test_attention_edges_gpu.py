@@ -44,3 +44,40 @@ def test_norm_without_eps(cuda_device, io, B, T, Hq, Hkv, dh):
     for x, dy, wx, n in ((q, dq, w[0], "q"), (k, dk, w[1], "k")):
         check_norm_grads(got, x, dy, wx, pos, rot, io, 0.0, n)
         assert all(torch.isfinite(got[m]).all() for m in ("d" + n, "dw_" + n))
+
+
+# ---------------------------------------------------------- what is not finite, who it reaches
+
+@pytest.mark.parametrize("B", [1, 40])                  # split over clusters, and resident blocks
+@pytest.mark.parametrize("dh,G", [(64, 1), (64, 2), (128, 1), (128, 2), (256, 2)])
+def test_nan_key_in_every_column(cuda_device, dh, G, B):
+    """A NaN in a key is the output and the log-sum of every query that sees it, whichever column
+    of a tile it has (some go through another 2^x) and whether the mask cuts the tile or not."""
+    T = 600
+    gen = torch.Generator().manual_seed(91)
+    q, k, v = (randn(gen, (B, T, h, dh), "bf16").to(cuda_device) for h in (2, 2 // G, 2 // G))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v)
+    for key in (0, 1, 16, 17, 20, 33, 49, 127, 128, 160):
+        k2 = k.clone()
+        k2[B - 1, key, 0, 5] = float("nan")
+        got, glse = rg.rglru_local_attn_fwd(q, k2, v)
+        seen = torch.zeros(B, T, 2, dtype=torch.bool, device=cuda_device)
+        seen[B - 1, key:, :G] = True                    # the query heads of key head 0
+        assert torch.isnan(got[seen]).all() and torch.isnan(glse.transpose(1, 2)[seen]).all(), key
+        assert torch.equal(got[~seen], out[~seen]), key
+        assert torch.equal(glse.transpose(1, 2)[~seen], lse.transpose(1, 2)[~seen]), key
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_nan_query_in_the_gradients(cuda_device, dh):
+    """The gradients of the keys that a query with a NaN sees are NaN, whichever row it is."""
+    T = 600
+    gen = torch.Generator().manual_seed(92)
+    q, k, v, dout = (randn(gen, (1, T, 1, dh), "bf16").to(cuda_device) for _ in range(4))
+    for t in (256, 257, 272, 273, 276, 599):
+        q2 = q.clone()
+        q2[0, t, 0, 5] = float("nan")
+        out, lse = rg.rglru_local_attn_fwd(q2, k, v)
+        g = rg.rglru_local_attn_bwd(q2, k, v, out, lse, dout)
+        assert torch.isnan(g["dq"][0, t]).all()
+        assert torch.isnan(g["dk"][0, :t + 1]).all() and torch.isnan(g["dv"][0, :t + 1]).all(), t
