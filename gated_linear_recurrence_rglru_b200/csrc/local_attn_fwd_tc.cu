@@ -226,7 +226,8 @@ __device__ __forceinline__ void join(const Params &prm, const Un &un, uint32_t t
             make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
     }
   }
-  if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * at) = make_float2(m, some ? l : 0.0f);
+  // (m = -inf: no key seen, or none with a score above -inf)
+  if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * at) = make_float2(m, some && m != -INFINITY ? l : 0.0f);
   cluster_sync();
   const int tid = threadIdx.x, parts = prm.parts, share = kRows / parts;
   const int x0 = static_cast<int>(cluster_ctarank()) * share;            // this block's rows
@@ -634,8 +635,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           continue;
         }
         top *= prm.c;
-        // (a NaN moves m too, and stays in it)
-        const float mn = top <= m + kSlack ? m : max2(top, m);
+        // (a NaN moves m too and stays in it, and a score of +inf makes it one: its weight
+        // would be inf - inf, which the polynomial does not show)
+        const float mn = top <= m + kSlack ? m : max2(top, m) + (top - top);
         if (__any_sync(0xFFFFFFFFu, mn != m)) {
           const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
           l *= f;
@@ -734,8 +736,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         bar_sync_softmax<256>();                               // the next unit's first tile writes there
       }
       if (wait(&all_done[q], nu & 1)) {
-        // (a row that sees a key has a weight of 1 at least; NaN scores leave l NaN)
-        const bool none = l == 0.0f;
+        // a row that sees no key, or none with a score above -inf (to which the polynomial
+        // gives 2^-126); NaN scores leave m and l NaN
+        const bool none = m == -INFINITY;
         const float inv = none ? 0.0f : 1.0f / l;
         __nv_bfloat16 *dst = out + out_row * DH + g * kOut;
 #pragma unroll 1

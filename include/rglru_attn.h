@@ -109,7 +109,8 @@ int rglru_qk_norm_rope_bwd(const void *q, const rglru_strides *q_strides, const 
  * window >= 0 (0: none), sinks >= 0, scale finite and positive.
  * What lies in key rows that no query of the call sees has no effect, whatever
  * it is. A NaN in q is that query's output, a NaN in k that of the queries that
- * see the key; a value row that some query sees is taken to be finite (one that
+ * see the key, and so is a score of +inf; a score of -inf counts as a hidden key.
+ * A value row that some query sees is taken to be finite (one that
  * is not may reach, with weight zero, queries of the same call that do not see
  * it). bf16 with dh 64, 128 or 256 runs on the tensor cores (weights rounded
  * to bf16 for the product with v), everything else in fp32 on CUDA cores.

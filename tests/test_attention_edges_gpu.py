@@ -81,3 +81,55 @@ def test_nan_query_in_the_gradients(cuda_device, dh):
         g = rg.rglru_local_attn_bwd(q2, k, v, out, lse, dout)
         assert torch.isnan(g["dq"][0, t]).all()
         assert torch.isnan(g["dk"][0, :t + 1]).all() and torch.isnan(g["dv"][0, :t + 1]).all(), t
+
+
+@pytest.mark.parametrize("io,dh,B", [("bf16", 64, 1), ("bf16", 64, 40), ("bf16", 128, 1), ("bf16", 128, 40),
+                                     ("bf16", 256, 1), ("bf16", 256, 40), ("bf16", 72, 1), ("f32", 64, 1)])
+def test_scores_of_minus_infinity_weigh_nothing(cuda_device, io, dh, B):
+    """A key whose score is -inf counts as one that is not seen, in every column; a query with no
+    other key gets zeros and -inf."""
+    T = 600
+    gen = torch.Generator().manual_seed(93)
+    q, k, v = (randn(gen, (B, T, 2, dh), io) for _ in range(3))
+    q[..., 0] = 1.0
+    k[0, :, 0, 0] = float("-inf")                       # all keys of a head
+    k[0, 130:, 1, 0] = float("-inf")                    # the keys from 130 on
+    q, k, v = (x.to(cuda_device) for x in (q, k, v))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v)
+    assert torch.all(out[0, :, 0] == 0) and torch.all(torch.isneginf(lse[0, 0]))
+    few = slice(130, T)                                 # those see keys 0 .. 129 of head 1
+    kk = torch.where(torch.isinf(k), torch.zeros_like(k), k)
+    ref, size, lref = whole_rows(f64(q[0, few, 1]), f64(kk[0, :130, 1]), f64(v[0, :130, 1]), dh ** -0.5)
+    es = base.score_error(q[0, few, 1], kk[0, :130, 1], dh, dh ** -0.5)
+    w = 2 * es + (T + 16) * 2 * U
+    close(out[0, few, 1], ref, w * size + (UB * (size + np.abs(ref)) if io == "bf16" else 0), "out")
+    close(lse[0, 1, few], lref, es + (T + 16) * 2 * U + 4 * U * np.abs(lref), "lse")
+
+
+def whole_rows(q, k, v, scale):
+    """Attention of every query over every key, in 64 bits."""
+    z = scale * (q @ k.T)
+    m = z.max(-1, keepdims=True)
+    p = np.exp(z - m)
+    l = p.sum(-1, keepdims=True)
+    return p / l @ v, p / l @ np.abs(v), (np.log(l) + m)[:, 0]
+
+
+@pytest.mark.parametrize("B", [1, 40])
+@pytest.mark.parametrize("io,dh", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_scores_of_infinity_are_nan(cuda_device, io, dh, B):
+    """A key whose score is +inf has no softmax: NaN for the queries that see it, in every column."""
+    T = 600
+    gen = torch.Generator().manual_seed(96)
+    q, k, v = (randn(gen, (B, T, 2, dh), io) for _ in range(3))
+    q[..., 0] = 1.0
+    q, k, v = (x.to(cuda_device) for x in (q, k, v))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v)
+    for key in (0, 17, 20, 160):
+        k2 = k.clone()
+        k2[B - 1, key, 1, 0] = float("inf")
+        got, glse = rg.rglru_local_attn_fwd(q, k2, v)
+        seen = torch.zeros(B, T, 2, dtype=torch.bool, device=cuda_device)
+        seen[B - 1, key:, 1] = True
+        assert torch.isnan(got[seen]).all() and torch.isnan(glse.transpose(1, 2)[seen]).all(), key
+        assert torch.equal(got[~seen], out[~seen])
