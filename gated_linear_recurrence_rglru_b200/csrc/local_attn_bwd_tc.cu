@@ -475,16 +475,17 @@ __device__ __forceinline__ void walk(const Params &prm, const CUtensorMap *mx, c
           v[c + 3] = ex2(v[c + 3]);
         }
         hide(v, bits, 0.0f);
-        // walked rows that nobody sees, zeroed before a product reads them
+        // walked rows that nobody sees, or that see nothing, zeroed before a product reads them
         bool dead = false;
         if (kKeys)
-          dead = t0 + kBN > nq && nq < p.T;
+          dead = (t0 + kBN > nq && nq < p.T) || t0 + off < 0;
         else
           dead = dead_keys(p, nk).any(t0, kBN);
         if (dead) {
           if (kFirst && kSecond && !wait(dp_full, i & 1)) break;
           if (!kFirst && !wait(&w_full[i % C::kNW], (i / C::kNW) & 1)) break;
-          const bool mine = tid < kBN && (kKeys ? t0 + tid >= nq : dead_keys(p, nk).in(t0 + tid));
+          const bool mine = tid < kBN && (kKeys ? t0 + tid >= nq || t0 + tid + off < 0
+                                                : dead_keys(p, nk).in(t0 + tid));
           if (mine)
             for (int c = 0; c < DH / 64; ++c)
               for (int e = 0; e < 8; ++e) {

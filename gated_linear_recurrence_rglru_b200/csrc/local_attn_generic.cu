@@ -25,15 +25,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Rows r0 .. r0+BT-1 of one head (row stride st) to dst[BT][pitch]; rows at or
-// past n, and columns dh .. 64*NC-1, as zeros. Rows outside [first, ...) too.
+// Rows r0 .. r0+BT-1 of one head (row stride st) to dst[BT][pitch]; rows before
+// first, at or past n, and columns dh .. 64*NC-1, as zeros.
 template <typename T, int BT, int NC>
-__device__ __forceinline__ void fill(float *dst, const T *src, long long st, int r0, int n, int dh) {
+__device__ __forceinline__ void fill(float *dst, const T *src, long long st, int r0, int n, int dh, int first = 0) {
   constexpr int W = NC * 64, kPitch = W + 4, kV = W / 4;
   for (int i = threadIdx.x; i < BT * kV; i += kThreads) {
     const int r = i / kV, c = (i % kV) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < n && c < dh) {
+    if (r0 + r >= first && r0 + r < n && c < dh) {
       const T *s = src + (r0 + r) * st + c;
       if constexpr (sizeof(T) == 4) {
         v = __ldg(reinterpret_cast<const float4 *>(s));
@@ -478,8 +478,9 @@ attn_dkv_generic_kernel(const AttnArgs p, const float *delta, const PiecePlan pl
     const T *dop = static_cast<const T *>(p.dout) + (static_cast<long long>(b) * p.T * p.Hq + h) * p.dh;
     const long long srow = (static_cast<long long>(b) * p.Hq + h) * p.T;
     __syncthreads();
-    fill<T, BT, NC>(qs, head_of<T>(p.q, b, h), p.q.st, q0, n.nq, p.dh);
-    fill<T, BT, NC>(dos, dop, static_cast<long long>(p.Hq) * p.dh, q0, n.nq, p.dh);
+    // (queries before -off see no key: their rows count as zeros, whatever they hold)
+    fill<T, BT, NC>(qs, head_of<T>(p.q, b, h), p.q.st, q0, n.nq, p.dh, -off);
+    fill<T, BT, NC>(dos, dop, static_cast<long long>(p.Hq) * p.dh, q0, n.nq, p.dh, -off);
     for (int i = threadIdx.x; i < BT; i += kThreads) {
       lses[i] = q0 + i < n.nq ? p.lse[srow + q0 + i] : 0.0f;
       deltas[i] = q0 + i < n.nq ? delta[srow + q0 + i] : 0.0f;

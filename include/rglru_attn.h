@@ -130,6 +130,12 @@ int rglru_local_attn_fwd(const void *q, const rglru_strides *q_strides, const vo
  *   rows past a sequence are left as they were).
  * Key heads shared by several query heads get the sum of their gradients, taken
  * in a fixed order: the same inputs give the same bits.
+ * As in the forward, rows past a sequence and keys that no query sees may hold
+ * anything, and so may q, out and dout of queries that see no key. All other rows
+ * are taken to be finite: one that is not reaches the gradients it has a part in,
+ * and may reach, with weight zero, others of its batch row and key head.
+ * bf16 with dh 64, 128 or 256 runs on the tensor cores (weights and score
+ * gradients rounded to bf16 for their products), everything else in fp32.
  */
 size_t rglru_local_attn_bwd_workspace_bytes(int B, int T, int S, int Hq, int Hkv, int dh,
                                             int window, int sinks, int io);

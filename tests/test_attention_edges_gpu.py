@@ -133,3 +133,23 @@ def test_scores_of_infinity_are_nan(cuda_device, io, dh, B):
         seen[B - 1, key:, 1] = True
         assert torch.isnan(got[seen]).all() and torch.isnan(glse.transpose(1, 2)[seen]).all(), key
         assert torch.equal(got[~seen], out[~seen])
+
+
+@pytest.mark.parametrize("io,dh,T,S", [("bf16", 64, 300, 173), ("bf16", 128, 150, 20), ("bf16", 256, 300, 173),
+                                       ("bf16", 72, 100, 61), ("f32", 64, 100, 61), ("f32", 256, 70, 33)])
+def test_queries_that_see_no_key_reach_no_gradient(cuda_device, io, dh, T, S):
+    """With S < T the first T - S queries see no key: whatever they and their dout hold, their out
+    is zero and the other rows' results are what they were."""
+    gen = torch.Generator().manual_seed(94)
+    q, dout = (randn(gen, (2, T, 4, dh), io).to(cuda_device) for _ in range(2))
+    k, v = (randn(gen, (2, S, 2, dh), io).to(cuda_device) for _ in range(2))
+    out, lse = rg.rglru_local_attn_fwd(q, k, v)
+    g = rg.rglru_local_attn_bwd(q, k, v, out, lse, dout)
+    q2, dout2 = q.clone(), dout.clone()
+    q2[:, :T - S], dout2[:, :T - S] = float("nan"), float("inf")
+    got, glse = rg.rglru_local_attn_fwd(q2, k, v)
+    assert torch.equal(got, out) and torch.equal(glse, lse)
+    assert torch.all(out[:, :T - S] == 0) and torch.all(torch.isneginf(lse[..., :T - S]))
+    again = rg.rglru_local_attn_bwd(q2, k, v, out, lse, dout2)
+    assert all(torch.equal(g[n], again[n]) for n in g)
+    assert torch.all(g["dq"][:, :T - S] == 0)
