@@ -15,6 +15,8 @@
 // A key whose page number is out of range is hidden (and reported).
 #include <math.h>
 
+#include <algorithm>
+
 #include "attn_kernels.h"
 #include "common.cuh"
 
@@ -154,7 +156,7 @@ paged_decode_kernel(const DecodeArgs p, const Parts parts, int slices) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Unit un = unit_of(p, slices, 16);
   const Keys ks = visible_keys(p, un.b);
-  const int u0 = un.c * parts.chunk, u1 = min(u0 + parts.chunk, ks.nk);
+  const int u0 = un.c * parts.chunk, u1 = u0 + min(parts.chunk, ks.nk - u0);   // (the sums stay below 2^31)
   const int G = p.Hq / p.Hkv, g = min(16, G - un.g0);
   const long long hrow = static_cast<long long>(un.b) * p.Hq + un.kvh * G + un.g0;
   if (u0 >= u1) {
@@ -192,8 +194,8 @@ paged_decode_kernel(const DecodeArgs p, const Parts parts, int slices) {
   // this warp's groups: u0 + 16 * (warp + 4 i)
   const int n = u1 - u0 > warp * 16 ? (u1 - u0 - warp * 16 + 63) / 64 : 0;
   auto row_of = [&](int i) -> long long {          // lanes 0..15: the group's cache rows
-    const int u = u0 + 16 * (warp + kDecWarps * i) + lane;
-    return (i < n && lane < 16 && u < u1) ? cache_row(p, un.b, ks, u) : -1;
+    const int x = 16 * (warp + kDecWarps * i) + lane;
+    return (i < n && lane < 16 && x < u1 - u0) ? cache_row(p, un.b, ks, u0 + x) : -1;
   };
   auto issue = [&](int i, long long row) {
     const int s = i % kStages;
@@ -393,7 +395,7 @@ paged_decode_generic_kernel(const DecodeArgs p, const Parts parts, int slices) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Unit un = unit_of(p, slices, kGenHeads);
   const Keys ks = visible_keys(p, un.b);
-  const int u0 = un.c * parts.chunk, u1 = min(u0 + parts.chunk, ks.nk);
+  const int u0 = un.c * parts.chunk, u1 = u0 + min(parts.chunk, ks.nk - u0);   // (the sums stay below 2^31)
   const int G = p.Hq / p.Hkv, g = min(kGenHeads, G - un.g0);
   const long long hrow = static_cast<long long>(un.b) * p.Hq + un.kvh * G + un.g0;
   if (u0 >= u1) {
@@ -419,8 +421,8 @@ paged_decode_generic_kernel(const DecodeArgs p, const Parts parts, int slices) {
   auto issue = [&](int i) {
     if (i < n) {
       // 8 threads a key
-      const int key = tid >> 3, u = u0 + i * kGenKeys + key;
-      const long long row = u < u1 ? cache_row(p, un.b, ks, u) : -1;
+      const int key = tid >> 3, x = i * kGenKeys + key;
+      const long long row = x < u1 - u0 ? cache_row(p, un.b, ks, u0 + x) : -1;
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, row >= 0);  // keys 4 warp .. +3, 8 bits each
       if (lane == 0) {
         const uint32_t bits = (m & 1u) | ((m >> 7) & 2u) | ((m >> 14) & 4u) | ((m >> 21) & 8u);
@@ -541,7 +543,7 @@ decode_join_kernel(const DecodeArgs p, const Parts parts) {
   const int b = blockIdx.x / p.Hq;
   const Keys ks = visible_keys(p, b);
   if (ks.nk == 0) return;                          // written by chunk 0's block
-  const int n = (ks.nk + parts.chunk - 1) / parts.chunk;
+  const int n = (ks.nk - 1) / parts.chunk + 1;
   const long long row = static_cast<long long>(blockIdx.x) * parts.chunks;
   float mm = -INFINITY;
   for (int c = tid; c < n; c += kJoinThreads) mm = fmaxf(mm, parts.ml[row + c].x);
@@ -630,7 +632,7 @@ Parts parts_of(const DecodeArgs &p, int io) {
   Parts r;
   r.o = nullptr;
   r.ml = nullptr;
-  r.chunk = static_cast<int>(chunk_of(chunks));
+  r.chunk = static_cast<int>(std::min(chunk_of(chunks), 1ll << 30));   // (offsets past its end stay below 2^31)
   r.chunks = static_cast<int>((most + r.chunk - 1) / r.chunk);
   return r;
 }

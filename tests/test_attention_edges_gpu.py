@@ -153,3 +153,27 @@ def test_queries_that_see_no_key_reach_no_gradient(cuda_device, io, dh, T, S):
     again = rg.rglru_local_attn_bwd(q2, k, v, out, lse, dout2)
     assert all(torch.equal(g[n], again[n]) for n in g)
     assert torch.all(g["dq"][:, :T - S] == 0)
+
+
+# ---------------------------------------------------------------- one token over a cache
+
+@pytest.mark.parametrize("io,dh,page,most", [("bf16", 8, 1 << 16, (1 << 15) - 1), ("bf16", 64, 1 << 16, (1 << 15) - 1),
+                                             ("bf16", 8, 1, 2 ** 31 - 1), ("bf16", 64, 1, 2 ** 31 - 1)])
+def test_paged_attn_decode_of_the_longest_tables(cuda_device, io, dh, page, most):
+    """A table that names nearly 2^31 keys, or all of those, every page but the last one the same:
+    equal scores, so that out is the mean of the values."""
+    last = 2.0 ** 31 / page                             # (the last page weighs as much as the others)
+    kc = torch.zeros(2, page, 1, dh, dtype=DT[io], device=cuda_device)
+    vc = torch.ones_like(kc)
+    vc[1] = last
+    table = torch.zeros(1, most, dtype=torch.int32, device=cuda_device)
+    table[0, -1] = 1
+    q = torch.ones(1, 1, dh, dtype=DT[io], device=cuda_device)
+    lens = torch.tensor([page * most], dtype=torch.int32, device=cuda_device)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    got = rg.rglru_paged_attn_decode(q, kc, vc, table, lens, dev_status=status)
+    ref = np.full((1, 1, dh), (most - 1 + last) / most)
+    # A block's sum of ones is a whole number below 2^24, exact; the last page adds equal numbers,
+    # up to 65536 times 32768, powers of two; their sum and the join's of up to 1024 parts round.
+    close(got, ref, (1100 * 2 * U + UB) * ref, "out")
+    assert int(status) == 0
