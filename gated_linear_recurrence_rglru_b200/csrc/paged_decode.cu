@@ -26,24 +26,22 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The visible keys of sequence b: u = 0 .. nk-1 stands for key u (u < head) or
-// u + jump.
+// u + jump. Keys past what the table names are hidden (and the length reported);
+// the window stays where the length puts it.
 struct Keys {
   int nk, head, jump;
 };
 
 __device__ __forceinline__ Keys visible_keys(const DecodeArgs &p, int b) {
-  int n = __ldg(p.lens + b);
-  const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
-  if (n > cap) {
-    if (p.dev_status && threadIdx.x == 0) atomicCAS(p.dev_status, 0, RGLRU_ERR_INVALID_ARG);
-    n = static_cast<int>(cap);
-  }
-  if (n < 0) n = 0;
-  Keys k = {n, n, 0};
+  const int n = __ldg(p.lens + b), cap = p.max_pages * p.page_size;
+  if (n > cap && p.dev_status && threadIdx.x == 0) atomicCAS(p.dev_status, 0, RGLRU_ERR_INVALID_ARG);
+  const int end = max(min(n, cap), 0);
+  Keys k = {end, end, 0};
   if (p.window > 0 && n > p.window) {
-    k.head = min(p.sinks, n - p.window);
-    k.nk = k.head + p.window;
-    k.jump = n - k.nk;
+    const int start = n - p.window;                // the window's first key
+    k.head = min(p.sinks, min(start, end));
+    k.nk = k.head + max(end - start, 0);
+    k.jump = start - k.head;
   }
   return k;
 }

@@ -177,3 +177,31 @@ def test_paged_attn_decode_of_the_longest_tables(cuda_device, io, dh, page, most
     # up to 65536 times 32768, powers of two; their sum and the join's of up to 1024 parts round.
     close(got, ref, (1100 * 2 * U + UB) * ref, "out")
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("io,dh", [("bf16", 128), ("f32", 64), ("bf16", 72)])
+@pytest.mark.parametrize("window,sinks", [(20, 3), (20, 0), (31, 40), (5, 2)])
+def test_paged_attn_decode_past_its_table(cuda_device, io, dh, window, sinks):
+    """A length past what its table names is reported, and the keys past it are hidden: the window
+    stays where the length puts it."""
+    page, most = 8, 4
+    gen = torch.Generator().manual_seed(95)
+    lens = [45, 33, 32, 70, 2 ** 31 - 1, 52, 20]
+    B, cap = len(lens), page * most
+    table = torch.randperm(B * most, generator=gen).view(B, most).to(torch.int32)
+    q = randn(gen, (B, 4, dh), io)
+    kc, vc = (randn(gen, (B * most, page, 2, dh), io) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    d = [x.to(cuda_device) for x in (q, kc, vc, table, torch.tensor(lens, dtype=torch.int32))]
+    got = rg.rglru_paged_attn_decode(*d, window=window, sinks=sinks, dev_status=status)
+    assert int(status) == 1
+    for b, n in enumerate(lens):
+        keys = [j for j in range(min(n, cap)) if j > n - 1 - window or j < sinks]
+        if not keys:
+            assert torch.all(got[b] == 0)
+            continue
+        at = [(int(table[b, j // page]), j % page) for j in keys]
+        k, v = (np.stack([f64(c[p, s]) for p, s in at])[None] for c in (kc, vc))
+        ref, size = orc.paged_decode(f64(q[b:b + 1]), k, v, np.zeros((1, 1), int), [len(keys)], 0, 0, dh ** -0.5)
+        w = 2 * base.score_error(q, torch.tensor(k), dh, dh ** -0.5) + (cap + 16) * 2 * U
+        close(got[b:b + 1], ref, w * size + (UB * (size + np.abs(ref)) if io == "bf16" else 0), b)
