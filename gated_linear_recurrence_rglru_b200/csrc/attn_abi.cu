@@ -53,10 +53,12 @@ bool view(const void *p, const rglru_strides *s, int B, int T, int H, int dh, in
     if (B > 1 && (d.batch < dh || d.batch % per16 != 0)) return false;
     if (T > 1 && (d.token < dh || d.token % per16 != 0)) return false;
     if (H > 1 && (d.head < dh || d.head % per16 != 0)) return false;
-    // a stride of 2^38 elements is past any device's memory; the sums below and
-    // the copies' 40-bit byte strides stay in range
+    // 2^38 elements are past any device's memory: no stride and no dimension's whole
+    // reach is longer, so that the sums below and the copies' 40-bit byte strides stay
+    // in range
     constexpr long long kMost = 1ll << 38;
-    if (d.batch > kMost || d.token > kMost || d.head > kMost) return false;
+    const auto far = [](long long stride, int n) { return stride > kMost / (n > 2 ? n - 1 : 1); };
+    if (far(d.batch, B) || far(d.token, T) || far(d.head, H)) return false;
   }
   *v = {p, d.batch, d.token, d.head};
   const long long last = (B - 1ll) * d.batch + (T - 1ll) * d.token + (H - 1ll) * d.head + dh;
