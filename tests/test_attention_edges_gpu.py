@@ -46,6 +46,20 @@ def test_norm_without_eps(cuda_device, io, B, T, Hq, Hkv, dh):
         assert all(torch.isfinite(got[m]).all() for m in ("d" + n, "dw_" + n))
 
 
+@pytest.mark.parametrize("io,fold", [("f32", 16), ("bf16", 64)])
+def test_weight_gradients_of_many_rows(cuda_device, io, fold):
+    """dw of millions of equal rows is off by no more than the few are (`fold` of them here) that a
+    lane adds up before it folds them into an exact sum: a rounding each, beside the root's 4 u, the
+    two products', the fold's and the store's."""
+    B, T, dh = 4, 1 << 20, 8
+    q = torch.ones(B, T, 1, dh, dtype=DT[io], device=cuda_device)
+    dq = torch.full_like(q, 1 / 3)
+    got = rg.rglru_qk_norm_rope_bwd(q, q.clone(), dq, dq.clone(), rot=0, eps=3.0)   # (root 1 / 2)
+    ref = np.full(dh, B * T * float(dq[0, 0, 0, 0]) / 2)
+    for n in ("dw_q", "dw_k"):
+        close(got[n], ref, (8 + fold) * U * ref, n)
+
+
 # ---------------------------------------------------------- what is not finite, who it reaches
 
 @pytest.mark.parametrize("B", [1, 40])                  # split over clusters, and resident blocks
