@@ -219,3 +219,96 @@ def test_paged_attn_decode_past_its_table(cuda_device, io, dh, window, sinks):
         ref, size = orc.paged_decode(f64(q[b:b + 1]), k, v, np.zeros((1, 1), int), [len(keys)], 0, 0, dh ** -0.5)
         w = 2 * base.score_error(q, torch.tensor(k), dh, dh ** -0.5) + (cap + 16) * 2 * U
         close(got[b:b + 1], ref, w * size + (UB * (size + np.abs(ref)) if io == "bf16" else 0), b)
+
+
+# ------------------------------------------------------- several units of work a block or warp
+
+MANY = [  # 370 units of work and more over the resident blocks of the forward
+    ("bf16", 4, 700, 700, 32, 16, 64, 200, 2, [700, 0, 513, 90], "slice"),
+    ("bf16", 4, 1000, 1000, 36, 12, 64, 0, 0, [1000, 300, 0, 640], "dense"),
+    ("bf16", 3, 900, 900, 40, 20, 128, 0, 0, None, "heads"),
+    ("bf16", 4, 600, 900, 30, 10, 128, 250, 140, None, "slice"),
+    ("bf16", 4, 600, 600, 20, 2, 256, 300, 3, [600, 431, 1, 600], "slice"),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_local_attn_of_many_units(cuda_device, case):
+    base.test_local_attn_fwd(cuda_device, case)
+
+
+@pytest.mark.parametrize("case", MANY[::2], ids=str)
+def test_local_attn_bwd_of_many_blocks(cuda_device, case):
+    base.test_local_attn_bwd(cuda_device, case)
+
+
+@pytest.mark.parametrize("case", [("bf16", 8, 1250, 10, 1, 64, 64, "slice", 0, True),
+                                  ("f32", 8, 1250, 3, 2, 128, 64, "heads", 9000, True),
+                                  ("bf16", 5, 1700, 4, 1, 256, 128, "slice", 70, False)], ids=str)
+def test_norms_of_many_tokens(cuda_device, case):
+    """More tokens than warps: each takes several, with all of a token's heads."""
+    base.test_qk_norm_rope_fwd(cuda_device, case)
+    base.test_qk_norm_rope_bwd(cuda_device, case)
+
+
+@pytest.mark.parametrize("io,Hq,Hkv,dh,window,sinks", [("bf16", 10, 1, 256, 100, 4), ("bf16", 4, 2, 64, 0, 0),
+                                                       ("f32", 4, 2, 64, 50, 1)])
+def test_paged_attn_decode_of_many_sequences(cuda_device, io, Hq, Hkv, dh, window, sinks):
+    lens = [(b * 37) % 331 for b in range(200)]
+    base.test_paged_attn_decode(cuda_device, (io, Hq, Hkv, dh, 16, lens, window, sinks, 22))
+
+
+# --------------------------------------------------------------- calls that are allowed, and odd
+
+@pytest.mark.parametrize("io,dh", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_lengths_out_of_range_are_clamped(cuda_device, io, dh):
+    gen = torch.Generator().manual_seed(97)
+    q, k, v, dout = (randn(gen, (4, 150, h, dh), io).to(cuda_device) for h in (4, 2, 2, 4))
+    got = []
+    for lens in ([-3, 2 ** 31 - 1, 0, 150], [0, 150, 0, 150]):
+        n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+        out, lse = rg.rglru_local_attn_fwd(q, k, v, window=40, sinks=1, lens=n)
+        got.append([out, lse, *rg.rglru_local_attn_bwd(q, k, v, out, lse, dout, window=40, sinks=1, lens=n).values()])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("io,Hq,Hkv,dh,window,sinks", [("bf16", 16, 4, 128, 0, 0), ("bf16", 10, 1, 256, 300, 4),
+                                                       ("f32", 4, 2, 64, 0, 0)])
+def test_paged_attn_decode_under_a_wide_table(cuda_device, io, Hq, Hkv, dh, window, sinks):
+    """A table for far more keys than the sequences have, its other entries anything; and lengths
+    below zero."""
+    case = (io, Hq, Hkv, dh, 16, [700, 0, 33, 512], window, sinks, 44)
+    q, kc, vc, table, lens = base.decode_inputs(case, 24)
+    wide = torch.randint(-2 ** 31, 2 ** 31 - 1, (4, 8192), generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    wide[:, :44] = table
+    lens[1] = -7
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    d = [x.to(cuda_device) for x in (q, kc, vc, wide, lens)]
+    got = rg.rglru_paged_attn_decode(*d, window=window, sinks=sinks, dev_status=status)
+    assert int(status) == 0 and torch.all(got[1] == 0)
+    scale = dh ** -0.5
+    ref, size = orc.paged_decode(f64(q), f64(kc), f64(vc), table.numpy(), lens.tolist(), window, sinks, scale)
+    w = 2 * base.score_error(q, kc, dh, scale) + (700 + 16) * 2 * U
+    close(got, ref, w * size + (UB * (size + np.abs(ref)) if io == "bf16" else 0), "out")
+
+
+@pytest.mark.parametrize("B,T,S,dh", [(2, 900, 900, 64), (1, 30, 3000, 128), (2, 700, 700, 256)])
+def test_two_calls_at_once(cuda_device, B, T, S, dh):
+    """Resident blocks, or clusters, of two calls on two streams share the GPU: each gets its bits."""
+    gen = torch.Generator().manual_seed(98)
+    sets = [[randn(gen, (B, n, h, dh), "bf16").to(cuda_device) for n, h in ((T, 20), (S, 2), (S, 2), (T, 20))]
+            for _ in range(2)]
+
+    def calls(x, stream=None):
+        q, k, v, dout = x
+        out, lse = rg.rglru_local_attn_fwd(q, k, v, window=S // 2, sinks=2, stream=stream)
+        g = rg.rglru_local_attn_bwd(q, k, v, out, lse, dout, window=S // 2, sinks=2, stream=stream)
+        return [out, lse, *g.values()]
+
+    ref = [calls(x) for x in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[calls(x, s) for x, s in zip(sets, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(a, b) for x, y in zip(pair, ref) for a, b in zip(x, y))
