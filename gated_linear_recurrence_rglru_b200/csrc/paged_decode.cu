@@ -604,7 +604,7 @@ int slices_of(const DecodeArgs &p, int io) {
 // their tables and window allow, in waves of resident blocks that share HBM (44
 // bytes a ns and SM; 60 for an SM that runs beside idle ones), and the most chunks
 // within 5 % of the best are taken: 128 sequences of 1028 visible 256-wide keys
-// get one chunk (three took 47 us, one 32), 4 sequences of 131072 keys, ragged,
+// get one chunk (three took 47 us, one 31), 4 sequences of 131072 keys, ragged,
 // get 74 rather than 37 (128 us, 146 with 37).
 Parts parts_of(const DecodeArgs &p, int io) {
   const long long cap = static_cast<long long>(p.max_pages) * p.page_size;

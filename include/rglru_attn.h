@@ -20,6 +20,7 @@
  * allocation and no state kept between calls), and
  *   - io is the storage type of every activation, weight and cache; statistics,
  *     log-sums, softmax and accumulators are float.
+ *   - Every size is 1 or more; a row without tokens is a length of 0.
  *   - Query head h reads key head h / (Hq / Hkv); Hq is a multiple of Hkv.
  *   - dh is a multiple of 8, at most 256.
  *   - Tensors with strides: element (b, t, h, d) lies at
@@ -31,7 +32,8 @@
  *   - dev_status (device int or NULL) as in rglru.h. A page number outside
  *     [0, num_pages), a position past max_pages * page_size or a length past
  *     what its table can name sets RGLRU_ERR_INVALID_ARG there; what it names is
- *     neither read nor written (a key is treated as hidden). The tensor-core
+ *     neither read nor written (a key is treated as hidden, and a window stays
+ *     where the length puts it). The tensor-core
  *     attention reports RGLRU_ERR_TIMEOUT when one of its bounded waits expires.
  */
 #ifndef RGLRU_B200_ATTN_H
@@ -54,7 +56,8 @@ typedef struct {
  *   positions (B, T)   int, any sign, or NULL for 0..T-1
  *   q_out, k_out       io, dense (written)
  * rot is the number of rotated dims: 0 <= rot <= dh, a multiple of 16. The angle
- * is formed modulo one turn in 64-bit integers, so far positions lose nothing.
+ * is formed modulo one turn in 64-bit integers, so far positions lose nothing;
+ * sine and cosine are good to 2^-21 for bf16 rows and to the last places for fp32.
  * base > 1 (base >= 1 allowed), eps >= 0, both finite.
  */
 int rglru_qk_norm_rope_fwd(const void *q, const rglru_strides *q_strides, const void *k,
@@ -72,7 +75,8 @@ int rglru_qk_norm_rope_fwd(const void *q, const rglru_strides *q_strides, const 
  *   page_table (B, max_pages) int; positions (B, T) int, required
  * A token at a negative position is padding: it is not read, its row of q_out
  * becomes zeros and no slot is written.
- * Two tokens of a call with the same slot leave either one's values there.
+ * Two tokens of a call with the same slot leave either one's values there, each
+ * 16 bytes of it for themselves.
  */
 int rglru_qk_norm_rope_append(const void *q, const rglru_strides *q_strides, const void *k,
                               const rglru_strides *k_strides, const void *v,
@@ -113,7 +117,8 @@ int rglru_qk_norm_rope_bwd(const void *q, const rglru_strides *q_strides, const 
  * A value row that some query sees is taken to be finite (one that
  * is not may reach, with weight zero, queries of the same call that do not see
  * it). bf16 with dh 64, 128 or 256 runs on the tensor cores (weights rounded
- * to bf16 for the product with v), everything else in fp32 on CUDA cores.
+ * to bf16 for the product with v, an eighth of them good to 2.6e-6 before that, in
+ * lse too), everything else in fp32 on CUDA cores.
  */
 int rglru_local_attn_fwd(const void *q, const rglru_strides *q_strides, const void *k,
                          const rglru_strides *k_strides, const void *v,
@@ -157,7 +162,9 @@ int rglru_local_attn_bwd(const void *q, const rglru_strides *q_strides, const vo
  *   out (B, Hq, dh) io, dense (written)
  * Only visible keys are read: pages that hold none may be absent (any entry).
  * The visible keys of a sequence are split over thread blocks when there are
- * few sequences, and the parts are joined in a fixed order.
+ * few sequences, and the parts are joined in a fixed order. bf16 with dh 64, 128
+ * or 256 runs on the tensor cores (weights rounded to bf16 for the product with
+ * v), everything else in fp32 on CUDA cores.
  */
 size_t rglru_paged_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int dh, int page_size,
                                                int max_pages, int window, int sinks, int io);

@@ -312,3 +312,16 @@ def test_two_calls_at_once(cuda_device, B, T, S, dh):
     torch.cuda.synchronize()
     for pair in got:
         assert all(torch.equal(a, b) for x, y in zip(pair, ref) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", range(8, 257, 8))
+def test_every_width(cuda_device, io, dh):
+    """Norm, rotation, attention, their backwards and the decode, for every width of a head."""
+    norm = (io, 2, 7, 3, 1, dh, dh // 16 * 16, "slice", 40, True)
+    base.test_qk_norm_rope_fwd(cuda_device, norm)
+    base.test_qk_norm_rope_bwd(cuda_device, norm)
+    attn = (io, 2, 70, 75, 2, 1, dh, 30, 2, None, "slice")
+    base.test_local_attn_fwd(cuda_device, attn)
+    base.test_local_attn_bwd(cuda_device, attn)
+    base.test_paged_attn_decode(cuda_device, (io, 3, 1, dh, 5, [40, 300], 50, 1, 60))
